@@ -1,10 +1,10 @@
 """Cases for the low-bit serving operators beside the QK-Norm projection: one
 attention block's path with 8-bit weights and activations and a 4-bit cache.
 
-    quant    qknorm_quant_rows_i8     rows to 8-bit integers, one scale a row
-    proj     qknorm_qkv_proj_w8a8     the QKV projection on 8-bit integers, QK-Norm in its epilogue
-    cache    qknorm_kv4_append/_gather  K and V of fused rows into a paged 4-bit cache, and out of it
-    attn     qknorm_kv4_attention     attention of fused rows' Q over that cache
+    quant    qknorm_quant_rows     rows to 8-bit integers, one scale a row
+    proj     qknorm_qkv_proj_quant     the QKV projection on 8-bit integers, QK-Norm in its epilogue
+    cache    qknorm_kv_append/_gather  K and V of fused rows into a paged 4-bit cache, and out of it
+    attn     qknorm_kv_attention     attention of fused rows' Q over that cache
 
 ``own`` false: elementary torch operations; true: the library's calls.
 
@@ -191,7 +191,7 @@ def prepare(c, seed):
         s["space"] = None
         if own:
             import qk_norm_amd as q
-            s["space"] = torch.empty(q.qknorm_qkv_proj_w8a8_workspace_bytes(T, hq, hkv, D), dtype=torch.uint8, device="cuda")
+            s["space"] = torch.empty(q.qknorm_qkv_proj_quant_workspace_bytes(T, hq, hkv, D), dtype=torch.uint8, device="cuda")
         return s
     if c["op"] == "cache":
         T = c["T"]
@@ -242,7 +242,7 @@ def prepare(c, seed):
              lse=torch.zeros(T, hq, dtype=torch.float32, device="cuda"), space=None)
     if own:
         import qk_norm_amd as q
-        s["space"] = torch.empty(q.qknorm_kv4_attention_workspace_bytes(T, B, width, hq, hkv, D), dtype=torch.uint8, device="cuda")
+        s["space"] = torch.empty(q.qknorm_kv_attention_workspace_bytes(T, B, width, hq, hkv, D), dtype=torch.uint8, device="cuda")
     return s
 
 
@@ -381,17 +381,17 @@ def _own(s):
     import qk_norm_amd as q
     c = s["case"]
     if c["op"] == "quant":
-        q.qknorm_quant_rows_i8(s["x"], s["q"], s["scale"])
+        q.qknorm_quant_rows(s["x"], s["q"], s["scale"])
         return {"q": s["q"], "scale": s["scale"]}
     if c["op"] == "proj":
-        q.qknorm_qkv_proj_w8a8(s["x"], s["x_scale"], s["w"], s["w_scale"], s["out"], c["hq"], c["hkv"], c["D"], s["gq"],
+        q.qknorm_qkv_proj_quant(s["x"], s["x_scale"], s["w"], s["w_scale"], s["out"], c["hq"], c["hkv"], c["D"], s["gq"],
                                s["gk"], EPS, plain=c["plain"], workspace=s["space"])
         return s["out"]
     if c["op"] == "cache":
-        q.qknorm_kv4_append(s["qkv"], c["hq"], c["hkv"], c["D"], s["cache"], s["slots"])
-        q.qknorm_kv4_gather(s["cache"], s["slots"], s["k"], s["v"], c["hkv"], c["D"])
+        q.qknorm_kv_append(s["qkv"], c["hq"], c["hkv"], c["D"], s["cache"], s["slots"])
+        q.qknorm_kv_gather(s["cache"], s["slots"], s["k"], s["v"], c["hkv"], c["D"])
         return {"k": s["k"], "v": s["v"]}
-    q.qknorm_kv4_attention(s["qkv"], s["cache"], s["table"], s["lens"], s["out"], c["hq"], c["hkv"], c["D"],
+    q.qknorm_kv_attention(s["qkv"], s["cache"], s["table"], s["lens"], s["out"], c["hq"], c["hkv"], c["D"],
                            q_starts=None if s["one"] else s["starts"], window=c["window"], lse=s["lse"],
                            workspace=s["space"])
     return {"out": s["out"], "lse": s["lse"]}
