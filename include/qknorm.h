@@ -263,6 +263,140 @@ int qknorm_qkv_proj_per_head_noalloc(const void *x, int64_t ldx, const void *w, 
                                      const void *gamma_k, float eps, int32_t flags, int32_t dtype,
                                      void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * 8-bit projection and 4-bit KV cache: one attention block's serving path,
+ *   qknorm_quant_rows -> qknorm_qkv_proj_quant -> qknorm_kv_append
+ *   -> qknorm_kv_attention.
+ * The conventions above hold (device pointers, no allocation, no
+ * synchronisation, host checks, T == 0 a no-op); `dtype` is QKNORM_BF16 or
+ * QKNORM_F16 unless said otherwise (others: QKNORM_E_UNSUPPORTED).  The
+ * stream's device must be the current one.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Rows to 8-bit integers with one scale a row:
+ *   scale[t] = max_j |x[t,j]| / 127                      (fp32)
+ *   q[t,j]   = 127 * x[t,j] / max_j |x[t,j]|, rounded to nearest, halfway to
+ *              even (the exact quotient decides)
+ * x [T, n] of `dtype`, pitch ldx; q [T, n] int8, pitch ldq; scale [T].  Rows
+ * whose largest magnitude is below 2^-100 get zeros and scale 0; rows with an
+ * infinity or a NaN get zeros and scale NaN, which makes every output that
+ * uses them NaN.  A projection weight [N, hidden] quantises the same way, one
+ * scale per output channel.
+ * Requires: x and q 16-byte aligned, n and ldq multiples of 16, ldx of 8; T
+ * below 2^24, n up to 2^24.  q and scale must not overlap x.
+ */
+int qknorm_quant_rows(const void *x, int64_t ldx, void *q, int64_t ldq, float *scale, int64_t T,
+                         int64_t n, int32_t dtype, void *stream);
+
+/*
+ * qknorm_qkv_proj_per_head on 8-bit integers:
+ *   qkv[t,n] = (sum_k x[t,k] * w[n,k]) * w_scale[n] * x_scale[t]
+ * with x [T, hidden] and w [N, hidden] int8 (pitches ldx, ldw in elements),
+ * x_scale [T] and w_scale [N] fp32; then per-head QK-Norm of Q and K heads
+ * (unless QKNORM_PROJ_PLAIN), in fp32, one rounding to `dtype` (qkv's and
+ * gamma's).  The integer sums are exact (int32); the two scales are applied in
+ * the order written.
+ * workspace: NULL, or device memory of workspace_bytes >=
+ * qknorm_qkv_proj_quant_workspace_bytes(T, hq, hkv, head_dim), 16-byte
+ * aligned, not shared by calls that can run at the same time: from 1 to 64
+ * tokens the weight is then split over many more blocks (int32 partials, a
+ * second launch adds them).  With and without it the integer sums are the
+ * same; a normalised output may differ in its last bit.
+ * Requires what qknorm_qkv_proj_per_head does, with ldx and ldw multiples of
+ * 16, hidden a multiple of 64 below 131072 (no int32 sum overflows), and
+ * the scales 4-byte aligned.
+ */
+int qknorm_qkv_proj_quant(const void *x, int64_t ldx, const float *x_scale, const void *w, int64_t ldw,
+                         const float *w_scale, void *qkv, int64_t ld, int64_t T, int64_t hidden,
+                         int32_t hq, int32_t hkv, int32_t head_dim, const void *gamma_q,
+                         const void *gamma_k, float eps, int32_t flags, int32_t dtype,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes of the form above for T tokens (0: none is used). */
+int64_t qknorm_qkv_proj_quant_workspace_bytes(int64_t T, int32_t hq, int32_t hkv, int32_t head_dim);
+
+/*
+ * The 4-bit KV cache.  A page holds QKNORM_KV_PAGE tokens' K and V of all
+ * hkv heads: hkv blocks of 64*head_dim + 256 bytes, page p at
+ * cache + p*page_stride.  A block:
+ *   K codes    byte t*head_dim/2 + j: dims 2j (low 4 bits) and 2j+1 of token t
+ *   V codes    byte 32*head_dim + 64*j + t: dims 2j and 2j+1 of token t
+ *   K scales   bf16 at byte 64*head_dim + 2t
+ *   V scales   bf16 at byte 64*head_dim + 128 + 2t
+ * A code is four-bit floating point (1 sign, 2 exponent, 1 fraction bits: 0,
+ * .5, 1, 1.5, 2, 3, 4, 6 and their negatives), and a value is code * scale.  One
+ * scale serves one head vector of one token: scale = max|x| / 6 rounded to
+ * bf16, code = x / scale rounded to nearest, halfway to the even code, at most
+ * 6.  A vector below 2^-100 throughout is stored as zeros with scale 0, one
+ * with an infinity or a NaN as zeros with scale NaN.
+ * head_dim 64, 128 or 256 (others: QKNORM_E_UNSUPPORTED); cache and
+ * page_stride (bytes, at least a page) 16-byte aligned.
+ */
+#define QKNORM_KV_PAGE 64
+
+/* hkv * (64*head_dim + 256); negative on error. */
+int64_t qknorm_kv_page_bytes(int32_t hkv, int32_t head_dim);
+
+/*
+ * Stores K and V of fused rows (qkv [T, ld]: hq Q heads, hkv K heads, hkv V
+ * heads; K normalised already) at slots[t] = page*64 + place (int64, 8-byte
+ * aligned).  A row whose slot is negative or at or past num_pages*64 is
+ * skipped.  Each slot may be named once in a call: a slot named by two rows
+ * ends up with bytes of either.
+ */
+int qknorm_kv_append(const void *qkv, int64_t T, int64_t ld, int32_t hq, int32_t hkv,
+                      int32_t head_dim, void *cache, int64_t num_pages, int64_t page_stride,
+                      const int64_t *slots, int32_t dtype, void *stream);
+
+/*
+ * The values held at slots[t] into k[t, h*head_dim + d] and v (pitches ldk,
+ * ldv; dtype QKNORM_F32, QKNORM_BF16 or QKNORM_F16): code * scale, rounded
+ * once.  Rows whose slot names no place are left as they are.  Slots may
+ * repeat.  k, v 16-byte aligned, pitches multiples of 16 bytes.
+ */
+int qknorm_kv_gather(const void *cache, int64_t num_pages, int64_t page_stride, const int64_t *slots,
+                      int64_t T, int32_t hkv, int32_t head_dim, void *k, int64_t ldk, void *v,
+                      int64_t ldv, int32_t dtype, void *stream);
+
+/*
+ * Causal attention of fused rows' Q heads over the 4-bit cache.
+ * Sequence b has seq_lens[b] tokens in the cache, token j at place j%64 of
+ * page page_table[b*table_stride + j/64] (entries past its length are not
+ * read).  Its rows are q_starts[b] .. q_starts[b+1]-1 of the T rows, its last
+ * tokens, already in the cache (q_starts NULL: T == B and row b alone): row i
+ * of n is token p = seq_lens[b] - n + i and sees tokens 0..p, with window > 0
+ * only p-window+1..p.  Query head h reads KV head h / (hq/hkv).
+ *   out[t,h,:] = sum_j softmax_j(scale * q.K_j) V_j,
+ *   lse[t,h]   = log sum_j exp(scale * q.K_j)        (NULL: not wanted)
+ * A row that sees no token gets zeros and lse = -infinity.  Rows of no
+ * sequence (before q_starts[0], past q_starts[B]) are left as they are.
+ * A page number outside [0, num_pages) hides its tokens.  Hidden tokens and
+ * what lies past a sequence's length may hold anything.  Softmax statistics and
+ * sums are fp32; weights are rounded to fp16 (11 bits) for the product with V.
+ * seq_lens and q_starts are read on the GPU (a captured graph may be replayed
+ * with others); lengths are taken within [0, 64*max_pages], row offsets within
+ * [0, T]; offsets must not decrease (else the rows concerned are undefined).
+ *
+ * qkv [T, ld] and out [T, ldo] (hq*head_dim columns used) 16-byte aligned,
+ * pitches multiples of 8 elements; other arrays 4-byte aligned; hq a multiple
+ * of hkv; scale finite (QKNORM_E_SHAPE); B <= 4096.  out, lse and workspace
+ * must not overlap the inputs.  workspace: 16-byte aligned, at least
+ * qknorm_kv_attention_workspace_bytes(T, B, max_pages, hq, hkv, head_dim)
+ * bytes, contents irrelevant on entry, not shared by calls that can run at the
+ * same time (replays of two captured graphs included).
+ */
+int qknorm_kv_attention(const void *qkv, int64_t T, int64_t ld, const void *cache, int64_t num_pages,
+                         int64_t page_stride, const int32_t *page_table, int64_t table_stride,
+                         int64_t max_pages, const int32_t *seq_lens, const int32_t *q_starts, int64_t B,
+                         void *out, int64_t ldo, float *lse, int32_t hq, int32_t hkv, int32_t head_dim,
+                         float scale, int32_t window, int32_t dtype, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+int64_t qknorm_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t max_pages, int32_t hq,
+                                             int32_t hkv, int32_t head_dim);
+
 /* Static description of a return code; never NULL. */
 const char *qknorm_strerror(int code);
 

@@ -41,11 +41,14 @@ QKNORM_E_EPS = -6
 QKNORM_E_HIP = -7
 
 QKNORM_PROJ_PLAIN = 1
+QKNORM_KV_PAGE = 64    # tokens a page of the 4-bit cache holds
 
 EXPORTED = ("qknorm_per_head", "qknorm_layerwise", "qknorm_partial_sumsq",
             "qknorm_apply_scalar", "qknorm_qkv_proj_per_head", "qknorm_qkv_proj_workspace_bytes",
-            "qknorm_qkv_proj_per_head_ws", "qknorm_qkv_proj_per_head_noalloc", "qknorm_strerror",
-            "qknorm_abi_version")
+            "qknorm_qkv_proj_per_head_ws", "qknorm_qkv_proj_per_head_noalloc", "qknorm_quant_rows",
+            "qknorm_qkv_proj_quant", "qknorm_qkv_proj_quant_workspace_bytes", "qknorm_kv_page_bytes",
+            "qknorm_kv_append", "qknorm_kv_gather", "qknorm_kv_attention",
+            "qknorm_kv_attention_workspace_bytes", "qknorm_strerror", "qknorm_abi_version")
 
 _lib = None
 
@@ -77,9 +80,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qknorm_qkv_proj_per_head_ws.argtypes = [P, I64, P, I64, P, I64, I64, I64, I32, I32, I32, P, P,
                                                 F, I32, I32, P, I64, P]
     lib.qknorm_qkv_proj_per_head_noalloc.argtypes = lib.qknorm_qkv_proj_per_head.argtypes
+    lib.qknorm_quant_rows.argtypes = [P, I64, P, I64, P, I64, I64, I32, P]
+    lib.qknorm_qkv_proj_quant.argtypes = [P, I64, P, P, I64, P, P, I64, I64, I64, I32, I32, I32, P, P, F, I32, I32,
+                                         P, I64, P]
+    lib.qknorm_kv_append.argtypes = [P, I64, I64, I32, I32, I32, P, I64, I64, P, I32, P]
+    lib.qknorm_kv_gather.argtypes = [P, I64, I64, P, I64, I32, I32, P, I64, P, I64, I32, P]
+    lib.qknorm_kv_attention.argtypes = [P, I64, I64, P, I64, I64, P, I64, I64, P, P, I64, P, I64, P, I32, I32, I32,
+                                         F, I32, I32, P, I64, P]
+    for name, args in (("qknorm_qkv_proj_quant_workspace_bytes", [I64, I32, I32, I32]),
+                       ("qknorm_kv_page_bytes", [I32, I32]),
+                       ("qknorm_kv_attention_workspace_bytes", [I64, I64, I64, I32, I32, I32])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = I64
     for name in ("qknorm_per_head", "qknorm_layerwise", "qknorm_partial_sumsq",
                  "qknorm_apply_scalar", "qknorm_qkv_proj_per_head", "qknorm_qkv_proj_per_head_ws",
-                 "qknorm_qkv_proj_per_head_noalloc", "qknorm_abi_version"):
+                 "qknorm_qkv_proj_per_head_noalloc", "qknorm_quant_rows", "qknorm_qkv_proj_quant",
+                 "qknorm_kv_append", "qknorm_kv_gather", "qknorm_kv_attention", "qknorm_abi_version"):
         getattr(lib, name).restype = I32
     lib.qknorm_strerror.argtypes = [ctypes.c_int]
     lib.qknorm_strerror.restype = ctypes.c_char_p
@@ -103,6 +119,11 @@ class _CtypesCalls:
         self.qkv_proj_per_head = lib.qknorm_qkv_proj_per_head
         self.qkv_proj_per_head_ws = lib.qknorm_qkv_proj_per_head_ws
         self.qkv_proj_per_head_noalloc = lib.qknorm_qkv_proj_per_head_noalloc
+        self.quant_rows = lib.qknorm_quant_rows
+        self.qkv_proj_quant = lib.qknorm_qkv_proj_quant
+        self.kv_append = lib.qknorm_kv_append
+        self.kv_gather = lib.qknorm_kv_gather
+        self.kv_attention = lib.qknorm_kv_attention
 
     @staticmethod
     def per_head_t(*_):
@@ -368,7 +389,209 @@ def qknorm_qkv_proj_per_head_noalloc(x, w, qkv, hq: int, hkv: int, head_dim: int
     _raise(rc, "qknorm_qkv_proj_per_head_noalloc")
 
 
-__all__ = ["qknorm_per_head", "qknorm_qkv_proj_per_head", "qknorm_qkv_proj_per_head_ws",
+# ------------------------------------------------- 8-bit and 4-bit operators --
+
+def _on(dev, fn, *args):
+    """The call with the tensors' device current (kernels are launched there)."""
+    import torch
+    if torch._C._cuda_getDevice() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _packed_rows(t, what, dev=None):
+    """(pointer, T, row width, row pitch) of a [T, ...] GPU tensor with packed rows."""
+    try:
+        T, ld, d = _rows(t)
+    except ValueError as e:
+        raise ValueError(str(e).replace("qkv", what)) from None
+    if dev is not None and d != dev:
+        raise ValueError("all tensors must be on the same GPU")
+    width = 1
+    for n in t.shape[1:]:
+        width *= n
+    return t.data_ptr(), T, width, ld
+
+
+def _vector(t, dev, dtype, n, what):
+    """Pointer of a contiguous tensor of n values of dtype."""
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} values")
+    return _ptr(t, dev)
+
+
+def _need_gpu(t, what):
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a GPU tensor (the library has no CPU path)")
+    return t.get_device()
+
+
+def qknorm_quant_rows(x, q, scale, stream=None) -> None:
+    """Rows of x to 8-bit integers, one scale a row:
+    scale[t] = max|x[t]| / 127, q[t, j] = round(127 * x[t, j] / max|x[t]|), halfway to even.
+
+    x [T, n] bfloat16 or float16, q [T, n] int8, scale [T] float32; n a multiple of 16.  For a
+    projection weight [N, hidden] this is one scale per output channel.
+    """
+    import torch
+    dev = _need_gpu(x, "x")
+    xp, ldx = _matrix(x, dev, "x")
+    qp, ldq = _matrix(q, dev, "q")
+    if q.dtype != torch.int8 or q.shape != x.shape:
+        raise ValueError("q must be an int8 tensor of x's shape")
+    sp = _vector(scale, dev, torch.float32, x.shape[0], "scale")
+    rc = _on(dev, _calls().quant_rows, xp, ldx, qp, ldq, sp, x.shape[0], x.shape[1], _dtype_code(x),
+             _stream(stream, dev))
+    _raise(rc, "qknorm_quant_rows")
+
+
+def qknorm_qkv_proj_quant_workspace_bytes(T: int, hq: int, hkv: int, head_dim: int) -> int:
+    """Bytes of workspace with which qknorm_qkv_proj_quant takes its form for few tokens (0: none)."""
+    n = int(load().qknorm_qkv_proj_quant_workspace_bytes(int(T), int(hq), int(hkv), int(head_dim)))
+    if n < 0:
+        _raise(n, "qknorm_qkv_proj_quant_workspace_bytes")
+    return n
+
+
+def _workspace(workspace, dev):
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    nbytes = workspace.numel() * workspace.element_size()
+    return (_ptr(workspace, dev), nbytes) if nbytes else (None, 0)
+
+
+def qknorm_qkv_proj_quant(x, x_scale, w, w_scale, qkv, hq: int, hkv: int, head_dim: int, gamma_q=None,
+                         gamma_k=None, eps: float = 1e-6, plain: bool = False, workspace=None,
+                         stream=None) -> None:
+    """qkv[:, :N] = (x @ w.T) * x_scale[:, None] * w_scale, each Q and K head RMS-normalised in the epilogue.
+
+    x [T, hidden] and w [N, hidden] int8 (N = (hq + 2*hkv) * head_dim), x_scale [T] and w_scale
+    [N] float32, as qknorm_quant_rows makes them; qkv [T, >= N] and gamma bfloat16 or float16.
+    The integer product is exact.  A workspace of qknorm_qkv_proj_quant_workspace_bytes(T, ...)
+    bytes (contiguous, of no other call meanwhile) speeds up 1 to 64 tokens; None is allowed.
+    """
+    import torch
+    dev = _need_gpu(qkv, "qkv")
+    xp, ldx = _matrix(x, dev, "x")
+    wp, ldw = _matrix(w, dev, "w")
+    op, ld = _matrix(qkv, dev, "qkv")
+    if x.dtype != torch.int8 or w.dtype != torch.int8:
+        raise ValueError("x and w must be int8")
+    if x.shape[0] != qkv.shape[0] or x.shape[1] != w.shape[1] or w.shape[0] != (hq + 2 * hkv) * head_dim:
+        raise ValueError("x [T, hidden], w [N, hidden] and qkv [T, >= N] do not match")
+    xs = _vector(x_scale, dev, torch.float32, x.shape[0], "x_scale")
+    ws = _vector(w_scale, dev, torch.float32, w.shape[0], "w_scale")
+    wsp, nbytes = _workspace(workspace, dev)
+    rc = _on(dev, _calls().qkv_proj_quant, xp, ldx, xs, wp, ldw, ws, op, ld, x.shape[0], x.shape[1], hq, hkv, head_dim,
+             None if plain else _gamma(gamma_q, qkv, dev), None if plain else _gamma(gamma_k, qkv, dev), eps,
+             QKNORM_PROJ_PLAIN if plain else 0, _dtype_code(qkv), wsp, nbytes, _stream(stream, dev))
+    _raise(rc, "qknorm_qkv_proj_quant")
+
+
+def qknorm_kv_page_bytes(hkv: int, head_dim: int) -> int:
+    """Bytes of one page (64 tokens' K and V of all hkv heads) of the 4-bit cache."""
+    n = int(load().qknorm_kv_page_bytes(int(hkv), int(head_dim)))
+    if n < 0:
+        _raise(n, "qknorm_kv_page_bytes")
+    return n
+
+
+def _cache(cache, dev, hkv, head_dim):
+    """(pointer, pages, bytes from page to page) of a uint8 [pages, ...] cache tensor."""
+    import torch
+    if cache.dtype != torch.uint8:
+        raise ValueError("cache must be a uint8 tensor")
+    p, pages, width, stride = _packed_rows(cache, "cache", dev)
+    if width != hkv * (64 * head_dim + 256):
+        raise ValueError(f"a page of cache must be {hkv * (64 * head_dim + 256)} bytes, not {width}")
+    return p, pages, stride
+
+
+def _slots(slots, dev, T):
+    import torch
+    return _vector(slots, dev, torch.int64, T, "slots")
+
+
+def qknorm_kv_append(qkv, hq: int, hkv: int, head_dim: int, cache, slots, stream=None) -> None:
+    """Store K and V of fused rows in the paged 4-bit cache.
+
+    qkv [T, >= (hq + 2*hkv) * head_dim] bfloat16 or float16; cache uint8 [pages, hkv, 64*head_dim
+    + 256]; slots [T] int64, page * 64 + place, each named once (a row whose slot is negative or past
+    the last page is skipped).
+    """
+    dev = _need_gpu(qkv, "qkv")
+    qp, T, _, ld = _packed_rows(qkv, "qkv")
+    cp, pages, stride = _cache(cache, dev, hkv, head_dim)
+    rc = _on(dev, _calls().kv_append, qp, T, ld, hq, hkv, head_dim, cp, pages, stride, _slots(slots, dev, T),
+             _dtype_code(qkv), _stream(stream, dev))
+    _raise(rc, "qknorm_kv_append")
+
+
+def qknorm_kv_gather(cache, slots, k, v, hkv: int, head_dim: int, stream=None) -> None:
+    """The K and V values held at slots [T], into k and v [T, hkv, head_dim] (float32, bfloat16 or
+    float16); rows whose slot names no place are left as they are."""
+    dev = _need_gpu(cache, "cache")
+    cp, pages, stride = _cache(cache, dev, hkv, head_dim)
+    kp, T, wk, ldk = _packed_rows(k, "k", dev)
+    vp, Tv, wv, ldv = _packed_rows(v, "v", dev)
+    if Tv != T or k.dtype != v.dtype or wk != hkv * head_dim or wv != wk:
+        raise ValueError("k and v must be [T, hkv, head_dim] of one dtype")
+    rc = _on(dev, _calls().kv_gather, cp, pages, stride, _slots(slots, dev, T), T, hkv, head_dim, kp, ldk, vp, ldv,
+             _dtype_code(k), _stream(stream, dev))
+    _raise(rc, "qknorm_kv_gather")
+
+
+def qknorm_kv_attention_workspace_bytes(T: int, B: int, max_pages: int, hq: int, hkv: int, head_dim: int) -> int:
+    """Bytes of workspace that qknorm_kv_attention needs for T rows of B sequences of up to max_pages pages."""
+    n = int(load().qknorm_kv_attention_workspace_bytes(int(T), int(B), int(max_pages), int(hq), int(hkv), int(head_dim)))
+    if n < 0:
+        _raise(n, "qknorm_kv_attention_workspace_bytes")
+    return n
+
+
+def qknorm_kv_attention(qkv, cache, page_table, seq_lens, out, hq: int, hkv: int, head_dim: int,
+                         scale: float | None = None, q_starts=None, window: int = 0, lse=None, workspace=None,
+                         stream=None) -> None:
+    """Causal attention of the rows' Q heads over the paged 4-bit cache.
+
+    qkv [T, >= hq * head_dim] bfloat16 or float16 (Q first); out [T, hq * head_dim] or [T, hq,
+    head_dim] of its dtype; cache as for qknorm_kv_append; page_table [B, max_pages] and seq_lens
+    [B] int32: sequence b's tokens are the first seq_lens[b] of its pages.  q_starts [B + 1] int32:
+    its rows are q_starts[b] .. q_starts[b+1] - 1, the last tokens of the cache (which holds
+    them already); None: row b alone.  A token sees itself and what is before it, with window > 0 the
+    last `window` tokens of that; a row that sees nothing gives zeros (lse minus infinity), rows
+    of no sequence are left as they are.  scale defaults to head_dim ** -0.5; lse [T, hq] float32
+    receives the natural log of each row's sum of exponentials.  workspace: a contiguous tensor of at
+    least qknorm_kv_attention_workspace_bytes(T, B, max_pages, hq, hkv, head_dim) bytes that no other
+    call uses meanwhile.
+    """
+    import torch
+    dev = _need_gpu(qkv, "qkv")
+    qp, T, width, ld = _packed_rows(qkv, "qkv")
+    cp, pages, stride = _cache(cache, dev, hkv, head_dim)
+    op, To, wo, ldo = _packed_rows(out, "out", dev)
+    if To != T or out.dtype != qkv.dtype or wo < hq * head_dim or width < hq * head_dim:
+        raise ValueError("out and qkv must be [T, >= hq * head_dim] of one dtype")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be an int32 [B, max_pages] tensor with contiguous rows")
+    B, max_pages = page_table.shape
+    ldt = max(page_table.stride(0), max_pages) if B <= 1 else page_table.stride(0)
+    lens = _vector(seq_lens, dev, torch.int32, B, "seq_lens")
+    starts = None if q_starts is None else _vector(q_starts, dev, torch.int32, B + 1, "q_starts")
+    lp = None if lse is None else _vector(lse, dev, torch.float32, T * hq, "lse")
+    wsp, nbytes = _workspace(workspace, dev)
+    rc = _on(dev, _calls().kv_attention, qp, T, ld, cp, pages, stride, _ptr(page_table, dev), ldt, max_pages, lens, starts,
+             B, op, ldo, lp, hq, hkv, head_dim, head_dim ** -0.5 if scale is None else scale, window, _dtype_code(qkv),
+             wsp, nbytes, _stream(stream, dev))
+    _raise(rc, "qknorm_kv_attention")
+
+
+__all__ = ["qknorm_quant_rows", "qknorm_qkv_proj_quant", "qknorm_qkv_proj_quant_workspace_bytes",
+           "qknorm_kv_page_bytes", "qknorm_kv_append", "qknorm_kv_gather", "qknorm_kv_attention",
+           "qknorm_kv_attention_workspace_bytes", "QKNORM_KV_PAGE", "qknorm_per_head", "qknorm_qkv_proj_per_head", "qknorm_qkv_proj_per_head_ws",
            "qknorm_qkv_proj_workspace_bytes", "qknorm_qkv_proj_per_head_noalloc", "qknorm_layerwise", "qknorm_partial_sumsq", "qknorm_apply_scalar",
            "strerror", "abi_version", "load", "QKNormError", "QKNORM_F32", "QKNORM_BF16", "QKNORM_F16",
            "QKNORM_FP8_E4M3"]

@@ -2,8 +2,8 @@
  *
  * Two kinds of call, both argument marshalling only (every step of the work
  * runs in libqknorm.so):
- * - per_head, layerwise, partial_sumsq, apply_scalar and the qkv_proj_per_head
- *   calls (plain, _ws, _noalloc) take the C ABI's arguments as Python ints and floats
+ * - per_head, layerwise, partial_sumsq, apply_scalar, the qkv_proj_per_head
+ *   calls (plain, _ws, _noalloc), quant_rows, qkv_proj_quant and the kv calls take the C ABI's arguments as Python ints and floats
  *   (pointers as ints, 0 or None for NULL), convert them to C values and call the library's
  *   extern "C" function, returning its int status.  They replace ctypes,
  *   whose per-call conversion of eleven or more arguments costs about a
@@ -182,6 +182,142 @@ static PyObject* f_qkv_proj_per_head_ws(PyObject* self, PyObject* const* a, Py_s
                                                      gk, eps, fl, dt, ws, wsb, st));
 }
 
+/* quant_rows(x, ldx, q, ldq, scale_p, T, width, dt, st) -> int */
+static PyObject* f_quant_rows(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  void *x, *q, *scale_p, *st;
+  int64_t ldx, ldq, T, width;
+  int32_t dt;
+  if (!nargs_ok(n, 9, "quant_rows")) return NULL;
+  if (as_ptr(a[0], &x) ||
+      as_i64(a[1], &ldx) ||
+      as_ptr(a[2], &q) ||
+      as_i64(a[3], &ldq) ||
+      as_ptr(a[4], &scale_p) ||
+      as_i64(a[5], &T) ||
+      as_i64(a[6], &width) ||
+      as_i32(a[7], &dt) ||
+      as_ptr(a[8], &st))
+    return NULL;
+  return PyLong_FromLong(qknorm_quant_rows(x, ldx, q, ldq, (float*)scale_p, T, width, dt, st));
+}
+
+/* qkv_proj_quant(x, ldx, x_scale, w, ldw, w_scale, qkv, ld, T, hidden, hq, hkv, d, gq, gk, eps, fl, dt, ws, wsb, st) -> int */
+static PyObject* f_qkv_proj_quant(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  void *x, *x_scale, *w, *w_scale, *qkv, *gq, *gk, *ws, *st;
+  int64_t ldx, ldw, ld, T, hidden, wsb;
+  int32_t hq, hkv, d, fl, dt;
+  float eps;
+  if (!nargs_ok(n, 21, "qkv_proj_quant")) return NULL;
+  if (as_ptr(a[0], &x) ||
+      as_i64(a[1], &ldx) ||
+      as_ptr(a[2], &x_scale) ||
+      as_ptr(a[3], &w) ||
+      as_i64(a[4], &ldw) ||
+      as_ptr(a[5], &w_scale) ||
+      as_ptr(a[6], &qkv) ||
+      as_i64(a[7], &ld) ||
+      as_i64(a[8], &T) ||
+      as_i64(a[9], &hidden) ||
+      as_i32(a[10], &hq) ||
+      as_i32(a[11], &hkv) ||
+      as_i32(a[12], &d) ||
+      as_ptr(a[13], &gq) ||
+      as_ptr(a[14], &gk) ||
+      as_f32(a[15], &eps) ||
+      as_i32(a[16], &fl) ||
+      as_i32(a[17], &dt) ||
+      as_ptr(a[18], &ws) ||
+      as_i64(a[19], &wsb) ||
+      as_ptr(a[20], &st))
+    return NULL;
+  return PyLong_FromLong(qknorm_qkv_proj_quant(x, ldx, (const float*)x_scale, w, ldw, (const float*)w_scale, qkv, ld, T, hidden, hq, hkv, d, gq, gk, eps, fl, dt, ws, wsb, st));
+}
+
+/* kv_append(qkv, T, ld, hq, hkv, d, cache, pages, stride, slots, dt, st) -> int */
+static PyObject* f_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  void *qkv, *cache, *slots, *st;
+  int64_t T, ld, pages, stride;
+  int32_t hq, hkv, d, dt;
+  if (!nargs_ok(n, 12, "kv_append")) return NULL;
+  if (as_ptr(a[0], &qkv) ||
+      as_i64(a[1], &T) ||
+      as_i64(a[2], &ld) ||
+      as_i32(a[3], &hq) ||
+      as_i32(a[4], &hkv) ||
+      as_i32(a[5], &d) ||
+      as_ptr(a[6], &cache) ||
+      as_i64(a[7], &pages) ||
+      as_i64(a[8], &stride) ||
+      as_ptr(a[9], &slots) ||
+      as_i32(a[10], &dt) ||
+      as_ptr(a[11], &st))
+    return NULL;
+  return PyLong_FromLong(qknorm_kv_append(qkv, T, ld, hq, hkv, d, cache, pages, stride, (const int64_t*)slots, dt, st));
+}
+
+/* kv_gather(cache, pages, stride, slots, T, hkv, d, k, ldk, v, ldv, dt, st) -> int */
+static PyObject* f_kv_gather(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  void *cache, *slots, *k, *v, *st;
+  int64_t pages, stride, T, ldk, ldv;
+  int32_t hkv, d, dt;
+  if (!nargs_ok(n, 13, "kv_gather")) return NULL;
+  if (as_ptr(a[0], &cache) ||
+      as_i64(a[1], &pages) ||
+      as_i64(a[2], &stride) ||
+      as_ptr(a[3], &slots) ||
+      as_i64(a[4], &T) ||
+      as_i32(a[5], &hkv) ||
+      as_i32(a[6], &d) ||
+      as_ptr(a[7], &k) ||
+      as_i64(a[8], &ldk) ||
+      as_ptr(a[9], &v) ||
+      as_i64(a[10], &ldv) ||
+      as_i32(a[11], &dt) ||
+      as_ptr(a[12], &st))
+    return NULL;
+  return PyLong_FromLong(qknorm_kv_gather(cache, pages, stride, (const int64_t*)slots, T, hkv, d, k, ldk, v, ldv, dt, st));
+}
+
+/* kv_attention(qkv, T, ld, cache, pages, stride, table, ldt, width, lens, starts, B, out, ldo, lse, hq, hkv, d, scale, window, dt, ws, wsb, st) -> int */
+static PyObject* f_kv_attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  void *qkv, *cache, *table, *lens, *starts, *out, *lse, *ws, *st;
+  int64_t T, ld, pages, stride, ldt, width, B, ldo, wsb;
+  int32_t hq, hkv, d, window, dt;
+  float scale;
+  if (!nargs_ok(n, 24, "kv_attention")) return NULL;
+  if (as_ptr(a[0], &qkv) ||
+      as_i64(a[1], &T) ||
+      as_i64(a[2], &ld) ||
+      as_ptr(a[3], &cache) ||
+      as_i64(a[4], &pages) ||
+      as_i64(a[5], &stride) ||
+      as_ptr(a[6], &table) ||
+      as_i64(a[7], &ldt) ||
+      as_i64(a[8], &width) ||
+      as_ptr(a[9], &lens) ||
+      as_ptr(a[10], &starts) ||
+      as_i64(a[11], &B) ||
+      as_ptr(a[12], &out) ||
+      as_i64(a[13], &ldo) ||
+      as_ptr(a[14], &lse) ||
+      as_i32(a[15], &hq) ||
+      as_i32(a[16], &hkv) ||
+      as_i32(a[17], &d) ||
+      as_f32(a[18], &scale) ||
+      as_i32(a[19], &window) ||
+      as_i32(a[20], &dt) ||
+      as_ptr(a[21], &ws) ||
+      as_i64(a[22], &wsb) ||
+      as_ptr(a[23], &st))
+    return NULL;
+  return PyLong_FromLong(qknorm_kv_attention(qkv, T, ld, cache, pages, stride, (const int32_t*)table, ldt, width, (const int32_t*)lens, (const int32_t*)starts, B, out, ldo, (float*)lse, hq, hkv, d, scale, window, dt, ws, wsb, st));
+}
+
 /* ------------------------------------------------------------------------
  * The common case of the binding's marshalling, on torch tensors: qkv a
  * contiguous [T, ...] GPU torch.Tensor (T > 0; not a subclass) of a dtype the
@@ -328,6 +464,11 @@ static PyMethodDef kMethods[] = {
      "qknorm_qkv_proj_per_head_ws"},
     {"qkv_proj_per_head_noalloc", (PyCFunction)(void (*)(void))f_qkv_proj_per_head_noalloc,
      METH_FASTCALL, "qknorm_qkv_proj_per_head_noalloc"},
+    {"quant_rows", (PyCFunction)(void (*)(void))f_quant_rows, METH_FASTCALL, "qknorm_quant_rows"},
+    {"qkv_proj_quant", (PyCFunction)(void (*)(void))f_qkv_proj_quant, METH_FASTCALL, "qknorm_qkv_proj_quant"},
+    {"kv_append", (PyCFunction)(void (*)(void))f_kv_append, METH_FASTCALL, "qknorm_kv_append"},
+    {"kv_gather", (PyCFunction)(void (*)(void))f_kv_gather, METH_FASTCALL, "qknorm_kv_gather"},
+    {"kv_attention", (PyCFunction)(void (*)(void))f_kv_attention, METH_FASTCALL, "qknorm_kv_attention"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_qknorm_fast",

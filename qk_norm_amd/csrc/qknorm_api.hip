@@ -88,7 +88,7 @@ int device_cus(int* cus) {
 int check_proj(const void* x, int64_t ldx, const void* w, int64_t ldw, void* qkv, int64_t ld,
                int64_t T, int64_t hidden, int32_t hq, int32_t hkv, int32_t head_dim,
                const void* gamma_q, const void* gamma_k, float eps, int32_t flags, int32_t dtype,
-               qknorm::ProjArgs* a, int64_t* n) {
+               qknorm::ProjArgs* a, int64_t* n, bool w8a8 = false) {
   int rc = check_common(dtype, eps, T, ld);
   if (rc) return rc;
   if (dtype != QKNORM_BF16 && dtype != QKNORM_F16) return QKNORM_E_UNSUPPORTED;
@@ -106,7 +106,9 @@ int check_proj(const void* x, int64_t ldx, const void* w, int64_t ldw, void* qkv
   if (norm && (rc = check_gamma(gamma_k, hkv, T))) return rc;
   if (touched && (!aligned16(x) || !aligned16(w) || !aligned16(qkv))) return QKNORM_E_ALIGN;
   // 16-byte row pitches: a multiple of 8 two-byte elements
-  if (ldx % 8 != 0 || ldw % 8 != 0 || ld % 8 != 0) return QKNORM_E_ALIGN;
+  // (16 one-byte elements for x and w of the 8-bit product)
+  const int step = w8a8 ? 16 : 8;
+  if (ldx % step != 0 || ldw % step != 0 || ld % 8 != 0) return QKNORM_E_ALIGN;
   // every pitch within 64 MiB before any product is formed from it (the
   // kernel's own limits, checked next, are tighter still)
   if (ld > kMaxPitchBytes / 2 || ldx > kMaxPitchBytes / 2 || ldw > kMaxPitchBytes / 2 ||
@@ -114,8 +116,41 @@ int check_proj(const void* x, int64_t ldx, const void* w, int64_t ldw, void* qkv
     return QKNORM_E_UNSUPPORTED;
   *a = qknorm::ProjArgs{x, ldx, w, ldw, qkv, ld, T, hidden, hq, hkv, head_dim, gamma_q, gamma_k,
                         eps, flags, dtype};
-  if (!qknorm::proj_shape_ok(*a)) return QKNORM_E_UNSUPPORTED;
+  if (!(w8a8 ? qknorm::w8a8_shape_ok(*a) : qknorm::proj_shape_ok(*a))) return QKNORM_E_UNSUPPORTED;
   *n = N;
+  return QKNORM_OK;
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+constexpr int64_t kMaxQuantRows = (INT64_C(1) << 24) - 1;    // a block a row: 2^32 threads a launch
+constexpr int64_t kMaxBatch = 4096;                          // sequences an attention call takes
+constexpr int64_t kMaxPages = INT64_C(1) << 40;
+
+bool kv4_head_dim(int32_t d) { return d == 64 || d == 128 || d == 256; }
+
+// The cache's own arguments, for the calls that read or write it.
+int check_cache(const void* cache, int64_t pages, int64_t page_stride, int32_t hkv, int32_t head_dim, bool touched) {
+  if (pages < 0 || page_stride < 0) return QKNORM_E_SHAPE;
+  if (pages > kMaxPages) return QKNORM_E_UNSUPPORTED;
+  const int64_t page = (int64_t)hkv * (64 * (int64_t)head_dim + 256);
+  if (pages > 1 && page_stride < page) return QKNORM_E_SHAPE;
+  if (pages > 0 && page_stride > (INT64_C(1) << 60) / pages) return QKNORM_E_UNSUPPORTED;
+  if (touched && pages > 0 && cache == nullptr) return QKNORM_E_NULLPTR;
+  if (!aligned16(cache) || page_stride % 16 != 0) return QKNORM_E_ALIGN;
+  return QKNORM_OK;
+}
+
+// The sizes of an attention call; every product formed later is bounded here.
+int check_attn(int64_t T, int64_t B, int64_t max_pages, int32_t hq, int32_t hkv, int32_t head_dim) {
+  if (T < 0 || B < 0 || max_pages < 0 || hq < 0 || hkv < 0 || head_dim <= 0) return QKNORM_E_SHAPE;
+  if (hq > 0 && (hkv == 0 || hq % hkv != 0)) return QKNORM_E_SHAPE;
+  if (!kv4_head_dim(head_dim) || hq >= (1 << 16) || hkv >= (1 << 16)) return QKNORM_E_UNSUPPORTED;
+  if (B > kMaxBatch || T > kMaxRows || T * hq >= kMaxHeadIndex) return QKNORM_E_UNSUPPORTED;
+  if (max_pages > (INT64_C(1) << 24)) return QKNORM_E_UNSUPPORTED;
+  if ((__int128)T * hq * head_dim >= ((__int128)1 << 34)) return QKNORM_E_UNSUPPORTED;   // threads that join splits
+  // pages visited, were every sequence as long as its table
+  if ((__int128)(T * hq / 16 + B * hkv + 1) * (max_pages + 1) >= ((__int128)1 << 40)) return QKNORM_E_UNSUPPORTED;
   return QKNORM_OK;
 }
 
@@ -295,6 +330,141 @@ int qknorm_qkv_proj_per_head_noalloc(const void* x, int64_t ldx, const void* w, 
   int cus = 0;
   if ((rc = device_cus(&cus))) return rc;
   return finish(qknorm::launch_qkv_proj(a, static_cast<hipStream_t>(stream), cus));
+}
+
+int qknorm_quant_rows(const void* x, int64_t ldx, void* q, int64_t ldq, float* scale, int64_t T, int64_t n,
+                         int32_t dtype, void* stream) {
+  if (!known_dtype(dtype)) return QKNORM_E_DTYPE;
+  if (dtype != QKNORM_BF16 && dtype != QKNORM_F16) return QKNORM_E_UNSUPPORTED;
+  if (T < 0 || n < 0 || ldx < n || ldq < n) return QKNORM_E_SHAPE;
+  if (T > kMaxQuantRows || n > (INT64_C(1) << 24) || ldx > kMaxPitchBytes / 2 || ldq > kMaxPitchBytes)
+    return QKNORM_E_UNSUPPORTED;
+  if (T > 0 && (scale == nullptr || (n > 0 && (x == nullptr || q == nullptr)))) return QKNORM_E_NULLPTR;
+  if (!aligned16(x) || !aligned16(q) || !aligned(scale, 4)) return QKNORM_E_ALIGN;
+  if (n % 16 != 0 || ldx % 8 != 0 || ldq % 16 != 0) return QKNORM_E_ALIGN;
+  if (T == 0) return QKNORM_OK;
+  const qknorm::QuantArgs a{x, ldx, q, ldq, scale, T, n, dtype};
+  return finish(qknorm::launch_quant_rows(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t qknorm_qkv_proj_quant_workspace_bytes(int64_t T, int32_t hq, int32_t hkv, int32_t head_dim) {
+  if (T < 0 || hq < 0 || hkv < 0 || head_dim <= 0) return QKNORM_E_SHAPE;
+  if (T > kMaxRows) return QKNORM_E_UNSUPPORTED;
+  const __int128 n_wide = ((__int128)hq + 2 * (__int128)hkv) * head_dim;
+  if (n_wide >= (INT64_C(1) << 24)) return QKNORM_E_UNSUPPORTED;
+  return qknorm::w8a8_workspace_bytes(T, (int64_t)n_wide);
+}
+
+int qknorm_qkv_proj_quant(const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
+                         const float* w_scale, void* qkv, int64_t ld, int64_t T, int64_t hidden, int32_t hq,
+                         int32_t hkv, int32_t head_dim, const void* gamma_q, const void* gamma_k, float eps,
+                         int32_t flags, int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  qknorm::W8a8Args a;
+  int64_t N = 0;
+  int rc = check_proj(x, ldx, w, ldw, qkv, ld, T, hidden, hq, hkv, head_dim, gamma_q, gamma_k, eps, flags, dtype,
+                      &a.p, &N, true);
+  if (rc) return rc;
+  if (T > 0 && N > 0 && (x_scale == nullptr || w_scale == nullptr)) return QKNORM_E_NULLPTR;
+  if (!aligned(x_scale, 4) || !aligned(w_scale, 4)) return QKNORM_E_ALIGN;
+  if (workspace_bytes < 0) return QKNORM_E_SHAPE;
+  const int64_t need = workspace != nullptr ? qknorm::w8a8_workspace_bytes(T, N) : 0;
+  if (need > 0) {
+    if (!aligned16(workspace)) return QKNORM_E_ALIGN;
+    if (workspace_bytes < need) return QKNORM_E_SHAPE;
+  }
+  if (T == 0 || N == 0) return QKNORM_OK;
+  a.x_scale = x_scale;
+  a.w_scale = w_scale;
+  int cus = 0;
+  if ((rc = device_cus(&cus))) return rc;
+  return finish(qknorm::launch_w8a8(a, need > 0 ? workspace : nullptr, static_cast<hipStream_t>(stream), cus));
+}
+
+int64_t qknorm_kv_page_bytes(int32_t hkv, int32_t head_dim) {
+  if (hkv < 0 || head_dim <= 0) return QKNORM_E_SHAPE;
+  if (!kv4_head_dim(head_dim) || hkv > (1 << 16)) return QKNORM_E_UNSUPPORTED;
+  return (int64_t)hkv * (64 * head_dim + 256);
+}
+
+int qknorm_kv_append(const void* qkv, int64_t T, int64_t ld, int32_t hq, int32_t hkv, int32_t head_dim, void* cache,
+                      int64_t num_pages, int64_t page_stride, const int64_t* slots, int32_t dtype, void* stream) {
+  int rc = check_common(dtype, 0.f, T, ld);
+  if (rc) return rc;
+  if (dtype != QKNORM_BF16 && dtype != QKNORM_F16) return QKNORM_E_UNSUPPORTED;
+  if (hq < 0 || hkv < 0 || head_dim <= 0) return QKNORM_E_SHAPE;
+  if (((__int128)hq + 2 * (__int128)hkv) * head_dim > ld) return QKNORM_E_SHAPE;
+  if (!kv4_head_dim(head_dim) || hkv >= (1 << 16)) return QKNORM_E_UNSUPPORTED;
+  const bool touched = T > 0 && hkv > 0;
+  if ((rc = check_cache(cache, num_pages, page_stride, hkv, head_dim, touched))) return rc;
+  if (touched && (qkv == nullptr || slots == nullptr)) return QKNORM_E_NULLPTR;
+  if (ld > kMaxPitchBytes / 2) return QKNORM_E_UNSUPPORTED;
+  if (!aligned16(qkv) || ld % 8 != 0 || !aligned(slots, 8)) return QKNORM_E_ALIGN;
+  if (T >= kMaxHeadIndex / 4) return QKNORM_E_UNSUPPORTED;
+  if (!touched) return QKNORM_OK;
+  const qknorm::Kv4AppendArgs a{qkv, ld, T, hq, hkv, head_dim, cache, num_pages, page_stride, slots, dtype};
+  return finish(qknorm::launch_kv4_append(a, static_cast<hipStream_t>(stream)));
+}
+
+int qknorm_kv_gather(const void* cache, int64_t num_pages, int64_t page_stride, const int64_t* slots, int64_t T,
+                      int32_t hkv, int32_t head_dim, void* k, int64_t ldk, void* v, int64_t ldv, int32_t dtype,
+                      void* stream) {
+  int rc = check_common(dtype, 0.f, T, 0);
+  if (rc) return rc;
+  if (dtype == QKNORM_FP8_E4M3) return QKNORM_E_UNSUPPORTED;
+  if (hkv < 0 || head_dim <= 0) return QKNORM_E_SHAPE;
+  const int64_t width = (int64_t)hkv * head_dim;
+  if (ldk < width || ldv < width) return QKNORM_E_SHAPE;
+  if (!kv4_head_dim(head_dim) || hkv >= (1 << 16)) return QKNORM_E_UNSUPPORTED;
+  const bool touched = T > 0 && hkv > 0;
+  if ((rc = check_cache(cache, num_pages, page_stride, hkv, head_dim, touched))) return rc;
+  if (touched && (k == nullptr || v == nullptr || slots == nullptr)) return QKNORM_E_NULLPTR;
+  const int es = esize_of(dtype);
+  if (ldk > kMaxPitchBytes / es || ldv > kMaxPitchBytes / es) return QKNORM_E_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v) || (ldk * es) % 16 != 0 || (ldv * es) % 16 != 0 || !aligned(slots, 8))
+    return QKNORM_E_ALIGN;
+  if (T >= kMaxHeadIndex / 4) return QKNORM_E_UNSUPPORTED;
+  if (!touched) return QKNORM_OK;
+  const qknorm::Kv4GatherArgs a{cache, num_pages, page_stride, slots, T, hkv, head_dim, k, ldk, v, ldv, dtype};
+  return finish(qknorm::launch_kv4_gather(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t qknorm_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t max_pages, int32_t hq, int32_t hkv,
+                                             int32_t head_dim) {
+  const int rc = check_attn(T, B, max_pages, hq, hkv, head_dim);
+  if (rc) return rc;
+  return qknorm::kv4_attn_workspace_bytes(T, B, max_pages, hq, hkv, head_dim);
+}
+
+int qknorm_kv_attention(const void* qkv, int64_t T, int64_t ld, const void* cache, int64_t num_pages,
+                         int64_t page_stride, const int32_t* page_table, int64_t table_stride, int64_t max_pages,
+                         const int32_t* seq_lens, const int32_t* q_starts, int64_t B, void* out, int64_t ldo,
+                         float* lse, int32_t hq, int32_t hkv, int32_t head_dim, float scale, int32_t window,
+                         int32_t dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  int rc = check_common(dtype, 0.f, T, ld);
+  if (rc) return rc;
+  if (dtype != QKNORM_BF16 && dtype != QKNORM_F16) return QKNORM_E_UNSUPPORTED;
+  if ((rc = check_attn(T, B, max_pages, hq, hkv, head_dim))) return rc;
+  if (!std::isfinite(scale) || window < 0 || workspace_bytes < 0) return QKNORM_E_SHAPE;
+  const int64_t width = (int64_t)hq * head_dim;
+  if (ld < width || ldo < width || (B > 1 && table_stride < max_pages) || table_stride < 0) return QKNORM_E_SHAPE;
+  if (q_starts == nullptr && T != B) return QKNORM_E_SHAPE;
+  const bool touched = T > 0 && B > 0 && hq > 0;
+  if ((rc = check_cache(cache, num_pages, page_stride, hkv, head_dim, touched))) return rc;
+  if (touched && (qkv == nullptr || out == nullptr || seq_lens == nullptr || (max_pages > 0 && page_table == nullptr)))
+    return QKNORM_E_NULLPTR;
+  if (ld > kMaxPitchBytes / 2 || ldo > kMaxPitchBytes / 2) return QKNORM_E_UNSUPPORTED;
+  if (!aligned16(qkv) || !aligned16(out) || ld % 8 != 0 || ldo % 8 != 0) return QKNORM_E_ALIGN;
+  if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(q_starts, 4) || !aligned(lse, 4)) return QKNORM_E_ALIGN;
+  const int64_t need = qknorm::kv4_attn_workspace_bytes(T, B, max_pages, hq, hkv, head_dim);
+  if (touched && need > 0) {
+    if (workspace == nullptr) return QKNORM_E_NULLPTR;
+    if (workspace_bytes < need) return QKNORM_E_SHAPE;
+  }
+  if (!aligned16(workspace)) return QKNORM_E_ALIGN;
+  if (!touched) return QKNORM_OK;
+  const qknorm::Kv4AttnArgs a{qkv, ld, T, cache, num_pages, page_stride, page_table, table_stride, max_pages, seq_lens,
+                              q_starts, B, out, ldo, lse, hq, hkv, head_dim, window, scale, dtype, workspace};
+  return finish(qknorm::launch_kv4_attn(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
