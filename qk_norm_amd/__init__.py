@@ -129,9 +129,7 @@ class _CtypesCalls:
     def per_head_t(*_):
         return None
 
-    @staticmethod
-    def layerwise_t(*_):
-        return None
+    layerwise_t = quant_rows_t = qkv_proj_quant_t = kv_append_t = kv_gather_t = kv_attention_t = per_head_t
 
 
 def _calls():
@@ -434,6 +432,12 @@ def qknorm_quant_rows(x, q, scale, stream=None) -> None:
     x [T, n] bfloat16 or float16, q [T, n] int8, scale [T] float32; n a multiple of 16.  For a
     projection weight [N, hidden] this is one scale per output channel.
     """
+    c = _calls_mod or _calls()
+    rc = c.quant_rows_t(x, q, scale, stream)
+    if rc is not None:           # the common case, read in C++
+        if rc:
+            _raise(rc, "qknorm_quant_rows")
+        return
     import torch
     dev = _need_gpu(x, "x")
     xp, ldx = _matrix(x, dev, "x")
@@ -441,7 +445,7 @@ def qknorm_quant_rows(x, q, scale, stream=None) -> None:
     if q.dtype != torch.int8 or q.shape != x.shape:
         raise ValueError("q must be an int8 tensor of x's shape")
     sp = _vector(scale, dev, torch.float32, x.shape[0], "scale")
-    rc = _on(dev, _calls().quant_rows, xp, ldx, qp, ldq, sp, x.shape[0], x.shape[1], _dtype_code(x),
+    rc = _on(dev, c.quant_rows, xp, ldx, qp, ldq, sp, x.shape[0], x.shape[1], _dtype_code(x),
              _stream(stream, dev))
     _raise(rc, "qknorm_quant_rows")
 
@@ -473,6 +477,13 @@ def qknorm_qkv_proj_quant(x, x_scale, w, w_scale, qkv, hq: int, hkv: int, head_d
     The integer product is exact.  A workspace of qknorm_qkv_proj_quant_workspace_bytes(T, ...)
     bytes (contiguous, of no other call meanwhile) speeds up 1 to 64 tokens; None is allowed.
     """
+    c = _calls_mod or _calls()
+    rc = c.qkv_proj_quant_t(x, x_scale, w, w_scale, qkv, hq, hkv, head_dim, gamma_q, gamma_k, eps, plain,
+                            workspace, stream)
+    if rc is not None:           # the common case, read in C++
+        if rc:
+            _raise(rc, "qknorm_qkv_proj_quant")
+        return
     import torch
     dev = _need_gpu(qkv, "qkv")
     xp, ldx = _matrix(x, dev, "x")
@@ -485,7 +496,7 @@ def qknorm_qkv_proj_quant(x, x_scale, w, w_scale, qkv, hq: int, hkv: int, head_d
     xs = _vector(x_scale, dev, torch.float32, x.shape[0], "x_scale")
     ws = _vector(w_scale, dev, torch.float32, w.shape[0], "w_scale")
     wsp, nbytes = _workspace(workspace, dev)
-    rc = _on(dev, _calls().qkv_proj_quant, xp, ldx, xs, wp, ldw, ws, op, ld, x.shape[0], x.shape[1], hq, hkv, head_dim,
+    rc = _on(dev, c.qkv_proj_quant, xp, ldx, xs, wp, ldw, ws, op, ld, x.shape[0], x.shape[1], hq, hkv, head_dim,
              None if plain else _gamma(gamma_q, qkv, dev), None if plain else _gamma(gamma_k, qkv, dev), eps,
              QKNORM_PROJ_PLAIN if plain else 0, _dtype_code(qkv), wsp, nbytes, _stream(stream, dev))
     _raise(rc, "qknorm_qkv_proj_quant")
@@ -522,10 +533,16 @@ def qknorm_kv_append(qkv, hq: int, hkv: int, head_dim: int, cache, slots, stream
     + 256]; slots [T] int64, page * 64 + place, each named once (a row whose slot is negative or past
     the last page is skipped).
     """
+    c = _calls_mod or _calls()
+    rc = c.kv_append_t(qkv, hq, hkv, head_dim, cache, slots, stream)
+    if rc is not None:           # the common case, read in C++
+        if rc:
+            _raise(rc, "qknorm_kv_append")
+        return
     dev = _need_gpu(qkv, "qkv")
     qp, T, _, ld = _packed_rows(qkv, "qkv")
     cp, pages, stride = _cache(cache, dev, hkv, head_dim)
-    rc = _on(dev, _calls().kv_append, qp, T, ld, hq, hkv, head_dim, cp, pages, stride, _slots(slots, dev, T),
+    rc = _on(dev, c.kv_append, qp, T, ld, hq, hkv, head_dim, cp, pages, stride, _slots(slots, dev, T),
              _dtype_code(qkv), _stream(stream, dev))
     _raise(rc, "qknorm_kv_append")
 
@@ -533,13 +550,19 @@ def qknorm_kv_append(qkv, hq: int, hkv: int, head_dim: int, cache, slots, stream
 def qknorm_kv_gather(cache, slots, k, v, hkv: int, head_dim: int, stream=None) -> None:
     """The K and V values held at slots [T], into k and v [T, hkv, head_dim] (float32, bfloat16 or
     float16); rows whose slot names no place are left as they are."""
+    c = _calls_mod or _calls()
+    rc = c.kv_gather_t(cache, slots, k, v, hkv, head_dim, stream)
+    if rc is not None:           # the common case, read in C++
+        if rc:
+            _raise(rc, "qknorm_kv_gather")
+        return
     dev = _need_gpu(cache, "cache")
     cp, pages, stride = _cache(cache, dev, hkv, head_dim)
     kp, T, wk, ldk = _packed_rows(k, "k", dev)
     vp, Tv, wv, ldv = _packed_rows(v, "v", dev)
     if Tv != T or k.dtype != v.dtype or wk != hkv * head_dim or wv != wk:
         raise ValueError("k and v must be [T, hkv, head_dim] of one dtype")
-    rc = _on(dev, _calls().kv_gather, cp, pages, stride, _slots(slots, dev, T), T, hkv, head_dim, kp, ldk, vp, ldv,
+    rc = _on(dev, c.kv_gather, cp, pages, stride, _slots(slots, dev, T), T, hkv, head_dim, kp, ldk, vp, ldv,
              _dtype_code(k), _stream(stream, dev))
     _raise(rc, "qknorm_kv_gather")
 
@@ -568,6 +591,13 @@ def qknorm_kv_attention(qkv, cache, page_table, seq_lens, out, hq: int, hkv: int
     least qknorm_kv_attention_workspace_bytes(T, B, max_pages, hq, hkv, head_dim) bytes that no other
     call uses meanwhile.
     """
+    c = _calls_mod or _calls()
+    rc = c.kv_attention_t(qkv, cache, page_table, seq_lens, out, hq, hkv, head_dim,
+                          head_dim ** -0.5 if scale is None else scale, q_starts, window, lse, workspace, stream)
+    if rc is not None:           # the common case, read in C++
+        if rc:
+            _raise(rc, "qknorm_kv_attention")
+        return
     import torch
     dev = _need_gpu(qkv, "qkv")
     qp, T, width, ld = _packed_rows(qkv, "qkv")
@@ -583,7 +613,7 @@ def qknorm_kv_attention(qkv, cache, page_table, seq_lens, out, hq: int, hkv: int
     starts = None if q_starts is None else _vector(q_starts, dev, torch.int32, B + 1, "q_starts")
     lp = None if lse is None else _vector(lse, dev, torch.float32, T * hq, "lse")
     wsp, nbytes = _workspace(workspace, dev)
-    rc = _on(dev, _calls().kv_attention, qp, T, ld, cp, pages, stride, _ptr(page_table, dev), ldt, max_pages, lens, starts,
+    rc = _on(dev, c.kv_attention, qp, T, ld, cp, pages, stride, _ptr(page_table, dev), ldt, max_pages, lens, starts,
              B, op, ldo, lp, hq, hkv, head_dim, head_dim ** -0.5 if scale is None else scale, window, _dtype_code(qkv),
              wsp, nbytes, _stream(stream, dev))
     _raise(rc, "qknorm_kv_attention")

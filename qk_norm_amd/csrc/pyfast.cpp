@@ -8,7 +8,7 @@
  *   extern "C" function, returning its int status.  They replace ctypes,
  *   whose per-call conversion of eleven or more arguments costs about a
  *   microsecond, a third of a decode-sized launch.
- * - per_head_t and layerwise_t take the binding's own arguments (torch
+ * - per_head_t, layerwise_t and the other _t calls take the binding's own arguments (torch
  *   tensors) and read from them what the binding's Python path would, through
  *   torch's C++ tensor API (no Python-level attribute calls, each of which
  *   costs about 0.1 us): the common case only, and None for anything else
@@ -18,6 +18,7 @@
 #include <Python.h>
 #include <stdint.h>
 
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/qknorm.h"
@@ -447,6 +448,183 @@ static PyObject* f_layerwise_t(PyObject* self, PyObject* const* a, Py_ssize_t n)
   return PyLong_FromLong(qknorm_layerwise(qkv, T, ld, wq, wk, gq, gk, eps, ns, code, st));
 }
 
+/* ---- the 8-bit and 4-bit operators on torch tensors (common case) --------
+ * Each reads what the binding's Python path would and returns None for
+ * anything it would not take as it is: that path then answers, with its
+ * messages. */
+
+/* a GPU tensor on dev (dev < 0: any, which becomes dev) */
+static const at::Tensor* gpu_tensor(PyObject* o, int64_t* dev) {
+  const at::Tensor* t = tensor_of(o);
+  if (!t || !t->is_cuda()) return NULL;
+  if (*dev < 0) *dev = t->get_device();
+  return t->get_device() == *dev ? t : NULL;
+}
+
+/* whether dev is the current device (kernels are launched there) */
+static int is_current(int64_t dev) {
+  return c10::impl::VirtualGuardImpl(c10::DeviceType::CUDA).getDevice().index() == dev;
+}
+
+/* [T, ...] with packed rows: 1 and (T, row width, pitch, ptr), 0 otherwise */
+static int rows_of(PyObject* o, int64_t* dev, const at::Tensor** tensor, int64_t* T, int64_t* width, int64_t* ld,
+                   void** ptr) {
+  const at::Tensor* t = gpu_tensor(o, dev);
+  if (!t || t->dim() < 2) return 0;
+  *T = t->size(0);
+  if (*T <= 0) return 0;
+  int64_t row = 1;
+  for (int64_t i = t->dim() - 1; i > 0; --i) {
+    if (t->size(i) != 1 && t->stride(i) != row) return 0;
+    row *= t->size(i);
+  }
+  *width = row;
+  *ld = *T > 1 || t->stride(0) > row ? t->stride(0) : row;
+  *ptr = t->data_ptr();
+  *tensor = t;
+  return 1;
+}
+
+/* a contiguous tensor of n values (n < 0: any number) of a type */
+static int vector_of(PyObject* o, int64_t* dev, c10::ScalarType type, int64_t n, void** ptr) {
+  const at::Tensor* t = gpu_tensor(o, dev);
+  if (!t || t->scalar_type() != type || !t->is_contiguous() || (n >= 0 && t->numel() != n)) return 0;
+  *ptr = t->data_ptr();
+  return 1;
+}
+
+/* None or a contiguous tensor, as bytes (none: NULL) */
+static int space_of(PyObject* o, int64_t* dev, void** ptr, int64_t* bytes) {
+  *ptr = NULL;
+  *bytes = 0;
+  if (o == Py_None) return 1;
+  const at::Tensor* t = gpu_tensor(o, dev);
+  if (!t || !t->is_contiguous()) return 0;
+  *bytes = t->numel() * (int64_t)t->element_size();
+  if (*bytes) *ptr = t->data_ptr();
+  return 1;
+}
+
+/* quant_rows_t(x, q, scale, stream) -> int or None */
+static PyObject* f_quant_rows_t(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!nargs_ok(n, 4, "quant_rows_t")) return NULL;
+  if (!g_raw_stream) Py_RETURN_NONE;
+  int64_t dev = -1, T, w, ldx, Tq, wq, ldq;
+  void *x, *q, *sc, *st;
+  const at::Tensor *tx, *tq;
+  if (!rows_of(a[0], &dev, &tx, &T, &w, &ldx, &x) || !rows_of(a[1], &dev, &tq, &Tq, &wq, &ldq, &q) || tx->dim() != 2 ||
+      tq->dim() != 2 || tq->scalar_type() != c10::ScalarType::Char || Tq != T || wq != w ||
+      !vector_of(a[2], &dev, c10::ScalarType::Float, T, &sc) || !is_current(dev))
+    Py_RETURN_NONE;
+  const int code = dtype_code(*tx);
+  if (code < 0) Py_RETURN_NONE;
+  if (stream_ptr(a[3], dev, &st)) return NULL;
+  return PyLong_FromLong(qknorm_quant_rows(x, ldx, q, ldq, (float*)sc, T, w, code, st));
+}
+
+/* qkv_proj_quant_t(x, x_scale, w, w_scale, qkv, hq, hkv, head_dim, gamma_q, gamma_k, eps, plain, workspace, stream) */
+static PyObject* f_qkv_proj_quant_t(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!nargs_ok(n, 14, "qkv_proj_quant_t")) return NULL;
+  if (!g_raw_stream) Py_RETURN_NONE;
+  int64_t dev = -1, T, K, ldx, N, Kw, ldw, To, wo, ldo, bytes;
+  void *x, *xs, *w, *ws, *out, *gq = NULL, *gk = NULL, *work, *st;
+  const at::Tensor *to, *tx, *tw;
+  int32_t hq, hkv, d;
+  float eps;
+  if (!rows_of(a[4], &dev, &to, &To, &wo, &ldo, &out) || !rows_of(a[0], &dev, &tx, &T, &K, &ldx, &x) ||
+      !rows_of(a[2], &dev, &tw, &N, &Kw, &ldw, &w) || to->dim() != 2 || tx->dim() != 2 || tw->dim() != 2 ||
+      tx->scalar_type() != c10::ScalarType::Char || tw->scalar_type() != c10::ScalarType::Char || To != T || Kw != K ||
+      !vector_of(a[1], &dev, c10::ScalarType::Float, T, &xs) || !vector_of(a[3], &dev, c10::ScalarType::Float, N, &ws) ||
+      !space_of(a[12], &dev, &work, &bytes) || (a[11] != Py_True && a[11] != Py_False) || !is_current(dev))
+    Py_RETURN_NONE;
+  const int code = dtype_code(*to), plain = a[11] == Py_True;
+  if (code < 0 || (!plain && (!gamma_ptr(a[8], code, dev, &gq) || !gamma_ptr(a[9], code, dev, &gk)))) Py_RETURN_NONE;
+  if (as_i32(a[5], &hq) || as_i32(a[6], &hkv) || as_i32(a[7], &d) || as_f32(a[10], &eps)) return NULL;
+  if (N != ((int64_t)hq + 2 * (int64_t)hkv) * d) Py_RETURN_NONE;
+  if (stream_ptr(a[13], dev, &st)) return NULL;
+  return PyLong_FromLong(qknorm_qkv_proj_quant(x, ldx, (const float*)xs, w, ldw, (const float*)ws, out, ldo, T, K, hq, hkv, d,
+                                               gq, gk, eps, plain ? QKNORM_PROJ_PLAIN : 0, code, work, bytes, st));
+}
+
+/* the cache: uint8 [pages, ...] of pages of hkv heads of d */
+static int cache_of(PyObject* o, int64_t* dev, int32_t hkv, int32_t d, int64_t* pages, int64_t* stride, void** ptr) {
+  const at::Tensor* t;
+  int64_t w;
+  return rows_of(o, dev, &t, pages, &w, stride, ptr) && t->scalar_type() == c10::ScalarType::Byte &&
+         w == (int64_t)hkv * (64 * (int64_t)d + 256);
+}
+
+/* kv_append_t(qkv, hq, hkv, head_dim, cache, slots, stream) -> int or None */
+static PyObject* f_kv_append_t(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!nargs_ok(n, 7, "kv_append_t")) return NULL;
+  if (!g_raw_stream) Py_RETURN_NONE;
+  int64_t dev = -1, T, w, ld, pages, stride;
+  void *qkv, *cache, *slots, *st;
+  const at::Tensor* t;
+  int32_t hq, hkv, d;
+  if (as_i32(a[1], &hq) || as_i32(a[2], &hkv) || as_i32(a[3], &d)) return NULL;
+  if (!rows_of(a[0], &dev, &t, &T, &w, &ld, &qkv) || dtype_code(*t) < 0 ||
+      !cache_of(a[4], &dev, hkv, d, &pages, &stride, &cache) ||
+      !vector_of(a[5], &dev, c10::ScalarType::Long, T, &slots) || !is_current(dev))
+    Py_RETURN_NONE;
+  const int code = dtype_code(*t);
+  if (stream_ptr(a[6], dev, &st)) return NULL;
+  return PyLong_FromLong(qknorm_kv_append(qkv, T, ld, hq, hkv, d, cache, pages, stride, (const int64_t*)slots, code, st));
+}
+
+/* kv_gather_t(cache, slots, k, v, hkv, head_dim, stream) -> int or None */
+static PyObject* f_kv_gather_t(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!nargs_ok(n, 7, "kv_gather_t")) return NULL;
+  if (!g_raw_stream) Py_RETURN_NONE;
+  int64_t dev = -1, T, wk, ldk, Tv, wv, ldv, pages, stride;
+  void *cache, *slots, *k, *v, *st;
+  const at::Tensor *tk, *tv;
+  int32_t hkv, d;
+  if (as_i32(a[4], &hkv) || as_i32(a[5], &d)) return NULL;
+  if (!cache_of(a[0], &dev, hkv, d, &pages, &stride, &cache) || !rows_of(a[2], &dev, &tk, &T, &wk, &ldk, &k) ||
+      !rows_of(a[3], &dev, &tv, &Tv, &wv, &ldv, &v) || Tv != T || wk != (int64_t)hkv * d || wv != wk ||
+      tk->scalar_type() != tv->scalar_type() || dtype_code(*tk) < 0 ||
+      !vector_of(a[1], &dev, c10::ScalarType::Long, T, &slots) || !is_current(dev))
+    Py_RETURN_NONE;
+  const int code = dtype_code(*tk);
+  if (stream_ptr(a[6], dev, &st)) return NULL;
+  return PyLong_FromLong(
+      qknorm_kv_gather(cache, pages, stride, (const int64_t*)slots, T, hkv, d, k, ldk, v, ldv, code, st));
+}
+
+/* kv_attention_t(qkv, cache, page_table, seq_lens, out, hq, hkv, head_dim, scale, q_starts, window, lse, workspace,
+ *                stream) -> int or None */
+static PyObject* f_kv_attention_t(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!nargs_ok(n, 14, "kv_attention_t")) return NULL;
+  if (!g_raw_stream) Py_RETURN_NONE;
+  int64_t dev = -1, T, w, ld, pages, stride, B, wt, ldt, To, wo, ldo, bytes;
+  void *qkv, *cache, *table, *lens, *starts = NULL, *out, *lse = NULL, *work, *st;
+  const at::Tensor *tq, *tt, *to;
+  int32_t hq, hkv, d, window;
+  float scale;
+  if (as_i32(a[5], &hq) || as_i32(a[6], &hkv) || as_i32(a[7], &d) || as_i32(a[10], &window) || as_f32(a[8], &scale))
+    return NULL;
+  if (!rows_of(a[0], &dev, &tq, &T, &w, &ld, &qkv) || dtype_code(*tq) < 0 ||
+      !cache_of(a[1], &dev, hkv, d, &pages, &stride, &cache) || !rows_of(a[2], &dev, &tt, &B, &wt, &ldt, &table) ||
+      tt->dim() != 2 || tt->scalar_type() != c10::ScalarType::Int ||
+      !vector_of(a[3], &dev, c10::ScalarType::Int, B, &lens) || !rows_of(a[4], &dev, &to, &To, &wo, &ldo, &out) ||
+      To != T || to->scalar_type() != tq->scalar_type() || wo < (int64_t)hq * d || w < (int64_t)hq * d ||
+      (a[9] != Py_None && !vector_of(a[9], &dev, c10::ScalarType::Int, B + 1, &starts)) ||
+      (a[11] != Py_None && !vector_of(a[11], &dev, c10::ScalarType::Float, T * hq, &lse)) ||
+      !space_of(a[12], &dev, &work, &bytes) || !is_current(dev))
+    Py_RETURN_NONE;
+  const int code = dtype_code(*tq);
+  if (stream_ptr(a[13], dev, &st)) return NULL;
+  return PyLong_FromLong(qknorm_kv_attention(qkv, T, ld, cache, pages, stride, (const int32_t*)table, ldt, wt,
+                                             (const int32_t*)lens, (const int32_t*)starts, B, out, ldo, (float*)lse, hq, hkv,
+                                             d, scale, window, code, work, bytes, st));
+}
+
 static PyMethodDef kMethods[] = {
     {"setup", (PyCFunction)(void (*)(void))f_setup, METH_FASTCALL,
      "hand over torch's current-raw-stream function and the torch.Tensor type"},
@@ -454,6 +632,16 @@ static PyMethodDef kMethods[] = {
      "qknorm_per_head on torch tensors (common case; None: use the Python path)"},
     {"layerwise_t", (PyCFunction)(void (*)(void))f_layerwise_t, METH_FASTCALL,
      "qknorm_layerwise on torch tensors (common case; None: use the Python path)"},
+    {"quant_rows_t", (PyCFunction)(void (*)(void))f_quant_rows_t, METH_FASTCALL,
+     "qknorm_quant_rows on torch tensors (common case; None: use the Python path)"},
+    {"qkv_proj_quant_t", (PyCFunction)(void (*)(void))f_qkv_proj_quant_t, METH_FASTCALL,
+     "qknorm_qkv_proj_quant on torch tensors (common case; None: use the Python path)"},
+    {"kv_append_t", (PyCFunction)(void (*)(void))f_kv_append_t, METH_FASTCALL,
+     "qknorm_kv_append on torch tensors (common case; None: use the Python path)"},
+    {"kv_gather_t", (PyCFunction)(void (*)(void))f_kv_gather_t, METH_FASTCALL,
+     "qknorm_kv_gather on torch tensors (common case; None: use the Python path)"},
+    {"kv_attention_t", (PyCFunction)(void (*)(void))f_kv_attention_t, METH_FASTCALL,
+     "qknorm_kv_attention on torch tensors (common case; None: use the Python path)"},
     {"per_head", (PyCFunction)(void (*)(void))f_per_head, METH_FASTCALL, "qknorm_per_head"},
     {"layerwise", (PyCFunction)(void (*)(void))f_layerwise, METH_FASTCALL, "qknorm_layerwise"},
     {"partial_sumsq", (PyCFunction)(void (*)(void))f_partial_sumsq, METH_FASTCALL, "qknorm_partial_sumsq"},

@@ -44,12 +44,12 @@ struct Kv4AttnK {
   const int32_t* starts;       // or null: one row a sequence
   uint8_t* out;
   float* lse;                  // or null
-  uint32_t* plan;              // pages a split, then each sequence's first partial slot
-  float* stat;                 // [slot][row] maximum (log2) and sum
+  uint32_t* plan;              // page visits a wave, then the count of them before each sequence
+  float* stat;                 // [slot][row]: maximum (log2) and sum; two slots a wave
   float* part;                 // [slot][row][D]
   int64_t pages, T;
   uint64_t ldq_bytes, ldo_bytes, page_stride, table_stride;
-  uint32_t max_pages, B, hq, hkv, group, window, target, min_chunk, max_slots;
+  uint32_t max_pages, B, hq, hkv, group, window, workers;
   float scale2;
 };
 

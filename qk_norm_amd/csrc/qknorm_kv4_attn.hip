@@ -23,12 +23,16 @@
 // relative to the largest seen by the wave, so the products stay in fp16's
 // range whatever V's magnitude.  Statistics and accumulators are fp32.
 //
-// Where there are few rows the pages of a sequence are split over blocks.
-// How many ways is decided on the GPU from the lengths there (they may change
-// between replays of a captured graph): every block works out the same plan.
-// A block's waves take its pages in turn and are joined through LDS; the
-// splits of a sequence leave fp32 partials in the workspace, which a second
-// launch joins in split order.
+// Work is counted in page visits: one page of one head for one tile of rows,
+// and kUnitCost more for each tile and head (a unit), about what starting and
+// ending it takes.  The plan is made on the GPU from the lengths there (they
+// may change between replays of a captured graph), the same by every block.
+// Where there are few units, all visits laid end to end are cut into equal
+// runs, one a wave, whatever sequences and heads they fall in: a wave
+// then takes the end of one unit's pages, some whole units, and the start of
+// another's, so that it leaves at most two partial results, in the workspace,
+// which a second launch joins in page order.  Where there are many, each is one
+// wave's.  Waves share nothing but the plan.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -45,6 +49,14 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr uint32_t kUnitCost = 6;   // page visits that starting and ending a unit counts as
+constexpr uint32_t kMinRun = 2;     // page visits a wave takes at least
+// What the registers of a kernel for D dims and QT row tiles allow, without
+// spills.  More waves hide more of the memory's latency and of the steps
+// from one unit to the next.
+constexpr int waves_per_simd(int d, int qt) {
+  return d * qt <= 64 ? 4 : (d * qt <= 128 && qt == 1 ? 3 : (d * qt <= 256 ? 2 : 1));
+}
 constexpr float kLazy = 8.f;        // powers of two a score may exceed the kept maximum by
 
 template <int DT>
@@ -133,119 +145,112 @@ __device__ __forceinline__ uint32_t seq_tiles(const Kv4AttnK& a, const Seq& s, u
 __device__ __forceinline__ uint32_t seq_pages(const Kv4AttnK& a, const Seq& s) {
   uint32_t p = (s.len + kKv4Tokens - 1) / kKv4Tokens;
   if (a.window) {
+    // (a tile's own rows span at most the sequence's)
     const uint64_t w = ((uint64_t)a.window + s.rows) / kKv4Tokens + 2;
     if (w < p) p = (uint32_t)w;
   }
-  return p;
+  return p > 0 ? p : 1;                               // (a tile that sees nothing still gives zeros)
 }
-__device__ __forceinline__ uint32_t seq_splits(uint32_t pages, uint32_t chunk) {
-  return pages <= chunk ? 1 : (pages + chunk - 1) / chunk;
-}
-
-__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t* red) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return red[0] + red[1] + red[2] + red[3];
-}
-
-// Fills items[0..B] and slots[0..B] with the running counts of work items
-// and of partial slots (items of sequences that are split), and returns the
-// pages a split takes.
-__device__ __forceinline__ uint32_t make_plan(const Kv4AttnK& a, uint32_t rt, uint32_t* items, uint32_t* slots,
-                                              uint32_t* red) {
+// Fills visits[0..B] and units[0..B] with the running counts of page visits
+// and of units (a row tile of one head).
+__device__ __forceinline__ void make_plan(const Kv4AttnK& a, uint32_t rt, uint32_t* visits, uint32_t* units,
+                                          uint32_t* red) {
   const uint32_t tid = threadIdx.x, lane = tid & 63;
-  uint64_t mine = 0;
-  for (uint32_t b = tid; b < a.B; b += 256) {
-    const Seq s = load_seq(a, b);
-    mine += (uint64_t)seq_tiles(a, s, rt) * seq_pages(a, s) * a.hkv;
-  }
-  // the total in units of 256 pages, rounded up per thread, fits 32 bits
-  const uint32_t units = block_sum((uint32_t)((mine + 255) / 256), red);
-  uint64_t chunk = ((uint64_t)units * 256 + a.target - 1) / a.target;
-  if (chunk < a.min_chunk) chunk = a.min_chunk;
-  uint32_t base_i = 0, base_s = 0;
+  uint32_t base_v = 0, base_u = 0;
   for (uint32_t b0 = 0; b0 < a.B; b0 += 256) {
     const uint32_t b = b0 + tid;
-    uint32_t ni = 0, ns = 0;
+    uint32_t nv = 0, nu = 0;
     if (b < a.B) {
       const Seq s = load_seq(a, b);
-      const uint32_t sp = seq_splits(seq_pages(a, s), (uint32_t)chunk);
-      ni = seq_tiles(a, s, rt) * a.hkv * sp;
-      ns = sp > 1 ? ni : 0;
+      nu = seq_tiles(a, s, rt) * a.hkv;
+      nv = nu * (seq_pages(a, s) + kUnitCost);
     }
-    uint32_t xi = ni, xs = ns;                       // inclusive scan over the wave
+    uint32_t xv = nv, xu = nu;                       // inclusive scan over the wave
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t ui = __shfl_up(xi, o), us = __shfl_up(xs, o);
-      if (lane >= (uint32_t)o) { xi += ui; xs += us; }
+      const uint32_t uv = __shfl_up(xv, o), uu = __shfl_up(xu, o);
+      if (lane >= (uint32_t)o) { xv += uv; xu += uu; }
     }
+    if (b0 != 0) __syncthreads();
+    if (lane == 63) { red[tid >> 6] = xv; red[4 + (tid >> 6)] = xu; }
     __syncthreads();
-    if (lane == 63) { red[tid >> 6] = xi; red[4 + (tid >> 6)] = xs; }
-    __syncthreads();
-    uint32_t pi = base_i, ps = base_s;
-    for (uint32_t w = 0; w < (tid >> 6); ++w) { pi += red[w]; ps += red[4 + w]; }
-    if (b < a.B) { items[b] = pi + xi - ni; slots[b] = ps + xs - ns; }
-    base_i += red[0] + red[1] + red[2] + red[3];
-    base_s += red[4] + red[5] + red[6] + red[7];
+    uint32_t pv = base_v, pu = base_u;
+    for (uint32_t w = 0; w < (tid >> 6); ++w) { pv += red[w]; pu += red[4 + w]; }
+    if (b < a.B) { visits[b] = pv + xv - nv; units[b] = pu + xu - nu; }
+    base_v += red[0] + red[1] + red[2] + red[3];
+    base_u += red[4] + red[5] + red[6] + red[7];
   }
-  if (tid == 0) { items[a.B] = base_i; slots[a.B] = base_s; }
+  if (tid == 0) { visits[a.B] = base_v; units[a.B] = base_u; }
   __syncthreads();
-  return (uint32_t)chunk;
 }
 
-// The largest b with items[b] <= i (items[0] = 0 <= i < items[B]).
-__device__ __forceinline__ uint32_t find(const uint32_t* items, uint32_t B, uint32_t i) {
+// Page visits a wave takes, or 0 where each unit is one wave's: where there
+// are two units a wave or more.
+__device__ __forceinline__ uint32_t run_length(const Kv4AttnK& a, uint32_t visits, uint32_t units) {
+  if (units >= 2 * a.workers) return 0;
+  const uint32_t per = visits / a.workers + (visits % a.workers != 0);
+  return per > kMinRun ? per : kMinRun;
+}
+
+// The largest b with count[b] <= i (count[0] = 0 <= i < count[B]).
+__device__ __forceinline__ uint32_t find(const uint32_t* count, uint32_t B, uint32_t i) {
   uint32_t lo = 0, hi = B;
   while (hi - lo > 1) {
     const uint32_t mid = (lo + hi) / 2;
-    if (items[mid] <= i) lo = mid; else hi = mid;
+    if (count[mid] <= i) lo = mid; else hi = mid;
   }
   return lo;
 }
 
 // ------------------------------------------------------------- main kernel --
 
-// What a wave holds of one page of one head, as loaded.
+// What a wave holds of one page of one head, as loaded: K of tile j's lanes'
+// tokens (KD dwords of codes each) and the K scales of the lane group's 16
+// tokens; V of dim pairs 16*jj + l%16 for those tokens, and their scales.
 template <int D>
-struct PageRegs {
-  static constexpr int KD = D / 32;
-  uint32_t k[4][KD];       // tile j: the lane's token, its KD dwords of codes
-  u32x4 v[D / 32];         // dim pair 16*jj + l%16: 16 tokens
-  u32x4 ks[2], vs[2];      // scales of the lane's 16 tokens
+struct PageK {
+  uint32_t k[4][D / 32];
+  u32x4 s[2];
+};
+template <int D>
+struct PageV {
+  u32x4 v[D / 32];
+  u32x4 s[2];
 };
 
-template <int D>
-__device__ __forceinline__ void load_page(PageRegs<D>& p, const uint8_t* __restrict__ base, uint32_t m, uint32_t g) {
+// A page of one head is one buffer (wave-uniform), so that a lane keeps three
+// offsets for all its loads (what is the same for all lanes goes in the scalar offset).
+template <int D, int kPagePolicy>
+__device__ __forceinline__ void load_k(PageK<D>& p, Rsrc page, uint32_t m, uint32_t g) {
   constexpr int KD = D / 32;
+  const uint32_t at = (16 * (m / 4) + m % 4) * (D / 2) + g * (D / 8);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t tok = 16 * (m / 4) + 4 * j + m % 4;
-    const uint8_t* q = base + tok * (D / 2) + g * (D / 8);
     if constexpr (KD == 2) {
-      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-      const u32x2 x = *reinterpret_cast<const u32x2*>(q);
+      const auto x = __builtin_amdgcn_raw_buffer_load_b64(page, at, 4 * j * (D / 2), kPagePolicy);
       p.k[j][0] = x[0];
       p.k[j][1] = x[1];
     } else {
 #pragma unroll
       for (int i = 0; i < KD / 4; ++i) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(q + 16 * i);
+        const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(page, at, 4 * j * (D / 2) + 16 * i, kPagePolicy);
 #pragma unroll
         for (int e = 0; e < 4; ++e) p.k[j][4 * i + e] = x[e];
       }
     }
   }
 #pragma unroll
-  for (int jj = 0; jj < D / 32; ++jj)
-    p.v[jj] = *reinterpret_cast<const u32x4*>(base + 32 * D + (16 * jj + m) * 64 + 16 * g);
+  for (int i = 0; i < 2; ++i) p.s[i] = __builtin_amdgcn_raw_buffer_load_b128(page, 32 * g, 64 * D + 16 * i, kPagePolicy);
+}
+
+template <int D, int kPagePolicy>
+__device__ __forceinline__ void load_v(PageV<D>& p, Rsrc page, uint32_t m, uint32_t g) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    p.ks[i] = *reinterpret_cast<const u32x4*>(base + 64 * D + 32 * g + 16 * i);
-    p.vs[i] = *reinterpret_cast<const u32x4*>(base + 64 * D + 128 + 32 * g + 16 * i);
-  }
+  for (int jj = 0; jj < D / 32; ++jj)
+    p.v[jj] = __builtin_amdgcn_raw_buffer_load_b128(page, 64 * m + 16 * g, 32 * D + 1024 * jj, kPagePolicy);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    p.s[i] = __builtin_amdgcn_raw_buffer_load_b128(page, 32 * g, 64 * D + 128 + 16 * i, kPagePolicy);
 }
 
 // The wave's running state over its pages.
@@ -256,12 +261,11 @@ struct State {
   float vref;                    // the largest V scale seen
 };
 
-template <int DT, int D, int QT, bool MASKED>
-__device__ __forceinline__ void use_page(const PageRegs<D>& p, const u32x4 (&qf)[QT][D / 32], State<D, QT>& st,
-                                         float scale2, uint32_t g, uint32_t tok0, const uint32_t (&lo)[QT],
-                                         const uint32_t (&hi)[QT]) {
+// Scores of a page (tile j's row 4g + r: token 16g + 4j + r), in powers of two.
+template <int DT, int D, int QT>
+__device__ __forceinline__ void score_page(const PageK<D>& p, const u32x4 (&qf)[QT][D / 32], float scale2,
+                                           f32x4 (&s)[QT][4]) {
   constexpr int KD = D / 32;
-  f32x4 s[QT][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -273,31 +277,59 @@ __device__ __forceinline__ void use_page(const PageRegs<D>& p, const u32x4 (&qf)
       for (int t = 0; t < QT; ++t) s[t][j] = AttnElem<DT>::mfma(kf, qf[t][i], s[t][j]);
     }
   }
-  // scales of token 16g + 4j + r: word 2j + r/2 of the lane's eight
-  float kc[4][4], vc[4][4];
+  // the scale of token 16g + 4j + r: half r%2 of word 2j + r/2 of the lane's eight
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint32_t kw = p.ks[j / 2][2 * (j % 2) + r / 2], vw = p.vs[j / 2][2 * (j % 2) + r / 2];
-      kc[j][r] = __uint_as_float(r % 2 ? kw & 0xFFFF0000u : kw << 16) * scale2;
-      vc[j][r] = __uint_as_float(r % 2 ? vw & 0xFFFF0000u : vw << 16);
-      if constexpr (MASKED) {
-        // tokens that no row sees may hold anything
-        const uint32_t tok = tok0 + 16 * g + 4 * j + r;
-        bool seen = false;
+      const uint32_t w = p.s[j / 2][2 * (j % 2) + r / 2];
+      const float k = __uint_as_float(r % 2 ? w & 0xFFFF0000u : w << 16) * scale2;
 #pragma unroll
-        for (int t = 0; t < QT; ++t) seen = seen || (tok >= lo[t] && tok < hi[t]);
-        if (!seen) vc[j][r] = 0.f;
-      }
+      for (int t = 0; t < QT; ++t) s[t][j][r] *= k;
     }
-  float vmax = 0.f;
+}
+
+// The page's part in the running maximum and sum, and its weights w for the
+// second product (tokens 8u + r and 8u + 4 + r of the lane's group).  `full`:
+// every row sees all of the page; else what a row does not see is taken out,
+// whatever it holds.
+template <int D, int QT>
+__device__ __forceinline__ void weigh_page(const PageV<D>& p, f32x4 (&s)[QT][4], State<D, QT>& st, bool full, uint32_t g,
+                                           uint32_t tok0, const uint32_t (&lo)[QT], const uint32_t (&hi)[QT],
+                                           u32x4 (&w)[QT][2]) {
+  auto hidden = [&](int t, int j, int r) {
+    const uint32_t tok = tok0 + 16 * g + 4 * j + r;
+    return !(tok >= lo[t] && tok < hi[t]);
+  };
+  float vc[4][4], vmax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t vw = p.s[j / 2][2 * (j % 2) + r / 2];
+      vc[j][r] = __uint_as_float(r % 2 ? vw & 0xFFFF0000u : vw << 16);
+    }
+  if (!full) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        bool none = true;
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          const bool h = hidden(t, j, r);
+          none = none && h;
+          if (h) s[t][j][r] = -INFINITY;
+        }
+        if (none) vc[j][r] = 0.f;
+      }
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int r = 0; r < 4; ++r) vmax = __builtin_fmaxf(vmax, vc[j][r]);
   vmax = row_max(vmax);
-  if constexpr (MASKED) {
+  if (!full) {
     // rows see different tokens, so the largest scale is taken over the wave
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) vmax = __builtin_fmaxf(vmax, __shfl_xor(vmax, o));
@@ -310,15 +342,7 @@ __device__ __forceinline__ void use_page(const PageRegs<D>& p, const u32x4 (&qf)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float y = s[t][j][r] * kc[j][r];
-        if constexpr (MASKED) {
-          const uint32_t tok = tok0 + 16 * g + 4 * j + r;
-          if (!(tok >= lo[t] && tok < hi[t])) y = -INFINITY;
-        }
-        s[t][j][r] = y;
-        x = __builtin_fmaxf(x, y);
-      }
+      for (int r = 0; r < 4; ++r) x = __builtin_fmaxf(x, s[t][j][r]);
     top[t] = row_max(x);
     grow = grow || top[t] > st.m[t] + kLazy;
   }
@@ -346,27 +370,40 @@ __device__ __forceinline__ void use_page(const PageRegs<D>& p, const u32x4 (&qf)
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int r = 0; r < 4; ++r) vc[j][r] *= vinv;
-  u32x4 w[QT][2];
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
     const float m = st.m[t] == -INFINITY ? 0.f : st.m[t];
     float l = 0.f;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float p0 = __builtin_amdgcn_exp2f(s[t][2 * u][r] - m), p1 = __builtin_amdgcn_exp2f(s[t][2 * u + 1][r] - m);
-        l += p0 + p1;
-        float w0 = p0 * vc[2 * u][r], w1 = p1 * vc[2 * u + 1][r];
-        if constexpr (MASKED) {
-          // a hidden token's scale may be NaN
-          if (s[t][2 * u][r] == -INFINITY) w0 = 0.f;
-          if (s[t][2 * u + 1][r] == -INFINITY) w1 = 0.f;
-        }
-        w[t][u][r] = pack16<kF16>(w0, w1);           // tokens 8u + r and 8u + 4 + r of the group
+        const float x = __builtin_amdgcn_exp2f(s[t][j][r] - m);
+        l += x;
+        s[t][j][r] = x * vc[j][r];
       }
     st.l[t] += l;
   }
+  if (!full) {
+    // (a hidden token's scale may be NaN)
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (hidden(t, j, r)) s[t][j][r] = 0.f;
+  }
+#pragma unroll
+  for (int t = 0; t < QT; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) w[t][u][r] = pack16<kF16>(s[t][2 * u][r], s[t][2 * u + 1][r]);
+}
+
+template <int D, int QT>
+__device__ __forceinline__ void add_page(const PageV<D>& p, const u32x4 (&w)[QT][2], State<D, QT>& st) {
 #pragma unroll
   for (int jj = 0; jj < D / 32; ++jj)
 #pragma unroll
@@ -384,219 +421,329 @@ __device__ __forceinline__ void use_page(const PageRegs<D>& p, const u32x4 (&qf)
     }
 }
 
-// LDS: the plan's counts (2 * (B + 1)), eight words of reductions, then the
-// waves' m and l ([4][RT] each) and one wave's output ([RT][D + 4]).
+// One unit's pages [off, off + seg): the results where that is all of them,
+// else a partial result in `slot`.
 template <int DT, int D, int QT>
-__global__ __launch_bounds__(256) void kv4_attn_kernel(Kv4AttnK a) {
+__device__ __forceinline__ void run_unit(const Kv4AttnK& a, const Seq& sq, uint32_t b, uint32_t tile, uint32_t head,
+                                         uint32_t off, uint32_t seg, bool whole, uint32_t slot) {
   constexpr uint32_t RT = 16 * QT;
-  constexpr int kPitch = D + 4;
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  float* const sm = reinterpret_cast<float*>(smem);
-  float* const sl = sm + 4 * RT;
-  float* const so = sl + 4 * RT;
-  uint32_t* const red = reinterpret_cast<uint32_t*>(so + RT * kPitch);
-  uint32_t* const items = red + 8;
-  uint32_t* const slots = items + a.B + 1;
-  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const uint32_t m16 = lane % 16, g = lane / 16;
+  // One row tile a sequence reads its pages once: streamed (nt), 10 % faster than
+  // through the caches (four caches of 131071 tokens: 104 against 115 us).
+  // Several share them (four prompts' 512 rows each: 98 us, streamed 110).
+  constexpr int kPolicy = QT == 1 ? 2 : 0;
+  const uint32_t lane = threadIdx.x & 63, m16 = lane % 16, g = lane / 16;
+  const uint32_t nrows = sq.rows * a.group;
+  const uint32_t r0 = tile * RT, r1 = r0 + RT < nrows ? r0 + RT : nrows;
+  if (r0 >= nrows) return;                            // (row offsets out of order)
+  // the tokens that row r of the tile sees: [lo, hi)
+  const uint32_t L = sq.len, n = sq.rows;
+  auto row_hi = [&](uint32_t r) {
+    const int64_t h = (int64_t)L - n + r / a.group + 1;
+    return (uint32_t)(h < 0 ? 0 : h);
+  };
+  auto row_lo = [&](uint32_t hi) { return a.window && hi > a.window ? hi - a.window : 0u; };
+  const uint32_t hi_first = row_hi(r0), hi_last = row_hi(r1 - 1);
+  const uint32_t lo_first = row_lo(hi_first), lo_last = row_lo(hi_last);
+  uint32_t p0 = lo_first / kKv4Tokens, p1 = (hi_last + kKv4Tokens - 1) / kKv4Tokens;
+  p0 += off;
+  p1 = seg < p1 - (p0 < p1 ? p0 : p1) ? p0 + seg : p1;
 
-  const uint32_t chunk = make_plan(a, RT, items, slots, red);
-  if (blockIdx.x == 0) {                              // for the launch that joins the splits
-    for (uint32_t b = tid; b <= a.B; b += 256) a.plan[1 + b] = slots[b];
-    if (tid == 0) a.plan[0] = chunk;
+  u32x4 qf[QT][D / 32];
+  uint32_t lo[QT], hi[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    uint32_t r = r0 + t * 16 + m16;
+    r = r < r1 ? r : r1 - 1;                          // rows past the end repeat the last and are not stored
+    const uint8_t* q = a.q + (uint64_t)(sq.start + r / a.group) * a.ldq_bytes +
+                       ((uint64_t)head * a.group + r % a.group) * D * 2 + g * (D / 4) * 2;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) qf[t][i] = load16(q + 16 * i);
+    hi[t] = row_hi(r);
+    lo[t] = row_lo(hi[t]);
   }
-  const uint32_t total = items[a.B];
-  for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
-    const uint32_t b = uniform(find(items, a.B, item));
-    const Seq sq = load_seq(a, b);
-    const uint32_t tiles = seq_tiles(a, sq, RT), splits = seq_splits(seq_pages(a, sq), chunk);
-    const uint32_t in = item - items[b];
-    const uint32_t tile = in % tiles, head = in / tiles % a.hkv, split = in / (tiles * a.hkv);
-    const uint32_t nrows = sq.rows * a.group;
-    const uint32_t r0 = tile * RT, r1 = r0 + RT < nrows ? r0 + RT : nrows;
-    if (r0 >= nrows) continue;                        // (row offsets out of order)
-    // the tokens that row r of the tile sees: [lo, hi)
-    const uint32_t L = sq.len, n = sq.rows;
-    auto row_hi = [&](uint32_t r) {
-      const int64_t h = (int64_t)L - n + r / a.group + 1;
-      return (uint32_t)(h < 0 ? 0 : h);
-    };
-    auto row_lo = [&](uint32_t hi) { return a.window && hi > a.window ? hi - a.window : 0u; };
-    const uint32_t hi_first = row_hi(r0), hi_last = row_hi(r1 - 1);
-    const uint32_t lo_first = row_lo(hi_first), lo_last = row_lo(hi_last);
-    uint32_t p0 = lo_first / kKv4Tokens, p1 = (hi_last + kKv4Tokens - 1) / kKv4Tokens;
-    const uint32_t per = (p1 - p0 + splits - 1) / splits;
-    p0 = p0 + split * per;
-    p1 = p0 + per < p1 ? p0 + per : p1;
 
-    u32x4 qf[QT][D / 32];
-    uint32_t lo[QT], hi[QT];
+  State<D, QT> st;
+  st.vref = 0x1p-126f;
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      uint32_t r = r0 + t * 16 + m16;
-      r = r < r1 ? r : r1 - 1;                        // rows past the end repeat the last and are not stored
-      const uint8_t* q = a.q + (uint64_t)(sq.start + r / a.group) * a.ldq_bytes +
-                         ((uint64_t)head * a.group + r % a.group) * D * 2 + g * (D / 4) * 2;
+  for (int t = 0; t < QT; ++t) {
+    st.m[t] = -INFINITY;
+    st.l[t] = 0.f;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) qf[t][i] = load16(q + 16 * i);
-      hi[t] = row_hi(r);
-      lo[t] = row_lo(hi[t]);
-    }
+    for (int jj = 0; jj < D / 32; ++jj) st.acc[t][jj][0] = st.acc[t][jj][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
 
-    State<D, QT> st;
-    st.vref = 0x1p-126f;
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      st.m[t] = -INFINITY;
-      st.l[t] = 0.f;
-#pragma unroll
-      for (int jj = 0; jj < D / 32; ++jj) st.acc[t][jj][0] = st.acc[t][jj][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // The next page's K is asked for as soon as this page's has been used, and
+  // its V likewise, so about a page a wave is in flight at all times without
+  // a second set of registers.  A page that is not there is read as page 0
+  // and counted as past every row's tokens.
+  const int32_t* const table = a.table + (uint64_t)b * a.table_stride;
+  const uint8_t* const cache = a.cache + (uint64_t)head * kv4_head_bytes(D);
+  auto page_id = [&](uint32_t pg) { return (int32_t)uniform((uint32_t)table[pg < p1 ? pg : p1 - 1]); };
+  auto there = [&](int32_t id) { return id >= 0 && id < a.pages; };
+  auto base = [&](int32_t id) {
+    return make_rsrc(cache + (uint64_t)(there(id) ? id : 0) * a.page_stride, kv4_head_bytes(D));
+  };
+  uint32_t pg = p0;
+  if (pg < p1) {
+    PageK<D> pk;
+    PageV<D> pv;
+    int32_t id = page_id(pg), next = page_id(pg + 1);
+    load_k<D, kPolicy>(pk, base(id), m16, g);
+    load_v<D, kPolicy>(pv, base(id), m16, g);
+    for (;;) {
+      const bool more = pg + 1 < p1;
+      const uint32_t tok0 = there(id) ? pg * kKv4Tokens : 0xFFFFFF00u;
+      const Rsrc nb = base(next);
+      const int32_t after = page_id(pg + 2);
+      f32x4 s[QT][4];
+      u32x4 w[QT][2];
+      score_page<DT, D, QT>(pk, qf, a.scale2, s);
+      if (more) load_k<D, kPolicy>(pk, nb, m16, g);
+      weigh_page<D, QT>(pv, s, st, tok0 >= lo_last && tok0 + kKv4Tokens <= hi_first, g, tok0, lo, hi, w);
+      add_page<D, QT>(pv, w, st);
+      if (!more) break;
+      load_v<D, kPolicy>(pv, nb, m16, g);
+      ++pg;
+      id = next;
+      next = after;
     }
-    const int32_t* const table = a.table + (uint64_t)b * a.table_stride;
-    const uint64_t head_off = (uint64_t)head * kv4_head_bytes(D);
-    for (uint32_t pg = p0 + wave; pg < p1; pg += 4) {
-      const int32_t id = (int32_t)uniform((uint32_t)table[pg]);
-      if (id < 0 || id >= a.pages) continue;          // a page that is not there hides its tokens
-      PageRegs<D> p;
-      load_page<D>(p, a.cache + (uint64_t)id * a.page_stride + head_off, m16, g);
-      const uint32_t tok0 = pg * kKv4Tokens;
-      if (tok0 >= lo_last && tok0 + kKv4Tokens <= hi_first)
-        use_page<DT, D, QT, false>(p, qf, st, a.scale2, g, tok0, lo, hi);
-      else
-        use_page<DT, D, QT, true>(p, qf, st, a.scale2, g, tok0, lo, hi);
-    }
+  }
 
-    // join the four waves
-    __syncthreads();
+  // (offsets from the tile's first row: below 2^31, rows being 64 MiB apart at most)
+  const Rsrc ro = make_rsrc(a.out + (uint64_t)(sq.start + r0 / a.group) * a.ldo_bytes, 0xFFFFFFFFu);
+  const Rsrc rp = make_rsrc(a.part + (uint64_t)slot * RT * D, RT * D * 4);
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      const float l = row_sum(st.l[t]);
-      if (g == 0) {
-        sm[wave * RT + t * 16 + m16] = st.m[t];
-        sl[wave * RT + t * 16 + m16] = l;
-      }
-    }
-    __syncthreads();
+  for (int t = 0; t < QT; ++t) {
+    const uint32_t r = r0 + t * 16 + m16;
+    const float l = row_sum(st.l[t]);
+    if (r >= r1) continue;
+    const float f = whole ? (l == 0.f ? 0.f : st.vref / l) : st.vref;
+    const uint32_t hd = head * a.group + r % a.group, ro_at = (r / a.group - r0 / a.group) * (uint32_t)a.ldo_bytes + hd * D * 2;
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) M = __builtin_fmaxf(M, sm[w * RT + t * 16 + m16]);
-      const float f = st.m[t] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.m[t] - M) * st.vref;
-#pragma unroll
-      for (int jj = 0; jj < D / 32; ++jj)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) st.acc[t][jj][h][r] *= f;
-    }
-    for (uint32_t w = 0; w < 4; ++w) {                // in wave order
-      if (wave == w) {
-#pragma unroll
-        for (int t = 0; t < QT; ++t)
-#pragma unroll
-          for (int jj = 0; jj < D / 32; ++jj)
-#pragma unroll
-            for (int r = 0; r < 4; r += 2) {
-              float* o = so + (t * 16 + m16) * kPitch + 32 * jj + 8 * g + 2 * r;
-              f32x4 x = {st.acc[t][jj][0][r], st.acc[t][jj][1][r], st.acc[t][jj][0][r + 1], st.acc[t][jj][1][r + 1]};
-              if (w != 0) x += *reinterpret_cast<const f32x4*>(o);
-              *reinterpret_cast<f32x4*>(o) = x;
-            }
-      }
-      __syncthreads();
-    }
-    // RT rows, D / 8 threads a row
-    const bool whole = splits == 1;
-    const uint32_t slot = slots[b] + in;
-    for (uint32_t i = tid; i < RT * (D / 8); i += 256) {
-      const uint32_t rr = i / (D / 8), c = i % (D / 8) * 8, r = r0 + rr;
-      if (r >= r1) continue;
-      float M = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) M = __builtin_fmaxf(M, sm[w * RT + rr]);
-      const float mm = M == -INFINITY ? 0.f : M;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) l += sl[w * RT + rr] * __builtin_amdgcn_exp2f(sm[w * RT + rr] - mm);
-      const f32x4 x0 = *reinterpret_cast<const f32x4*>(so + rr * kPitch + c);
-      const f32x4 x1 = *reinterpret_cast<const f32x4*>(so + rr * kPitch + c + 4);
+    for (int jj = 0; jj < D / 32; ++jj) {
+      // dims 32*jj + 8g .. + 7
+      const f32x4 (&o)[2] = st.acc[t][jj];
       if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const uint64_t row = sq.start + r / a.group;
-        const uint32_t hd = head * a.group + r % a.group;
-        const u32x4 o = {pack16<DT>(x0[0] * inv, x0[1] * inv), pack16<DT>(x0[2] * inv, x0[3] * inv),
-                         pack16<DT>(x1[0] * inv, x1[1] * inv), pack16<DT>(x1[2] * inv, x1[3] * inv)};
-        *reinterpret_cast<u32x4*>(a.out + row * a.ldo_bytes + ((uint64_t)hd * D + c) * 2) = o;
-        if (c == 0 && a.lse) a.lse[row * a.hq + hd] = l == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(l)) * kLn2;
-      } else if (slot < a.max_slots) {                // (always, for row offsets in order)
-        float* o = a.part + ((uint64_t)slot * RT + rr) * D + c;
-        *reinterpret_cast<f32x4*>(o) = x0;
-        *reinterpret_cast<f32x4*>(o + 4) = x1;
-        if (c == 0) {
-          a.stat[((uint64_t)slot * RT + rr) * 2] = M;
-          a.stat[((uint64_t)slot * RT + rr) * 2 + 1] = l;
-        }
+        const u32x4 v = {pack16<DT>(o[0][0] * f, o[1][0] * f), pack16<DT>(o[0][1] * f, o[1][1] * f),
+                         pack16<DT>(o[0][2] * f, o[1][2] * f), pack16<DT>(o[0][3] * f, o[1][3] * f)};
+        __builtin_amdgcn_raw_buffer_store_b128(v, ro, ro_at + g * 16, jj * 64, 0);
+      } else {
+        const f32x4 x = f32x4{o[0][0], o[1][0], o[0][1], o[1][1]} * f, y = f32x4{o[0][2], o[1][2], o[0][3], o[1][3]} * f;
+        const uint32_t at = m16 * D * 4 + g * 32, k = t * 16 * D * 4 + jj * 128;
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), rp, at, k, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), rp, at, k + 16, 0);
       }
     }
-    __syncthreads();
+    if (g == 0) {
+      if (!whole) {
+        const uint64_t at = (uint64_t)slot * RT + t * 16 + m16;
+        a.stat[at * 2] = st.m[t];
+        a.stat[at * 2 + 1] = l;
+      } else if (a.lse) {
+        a.lse[(uint64_t)(sq.start + r / a.group) * a.hq + hd] = l == 0.f ? -INFINITY : (st.m[t] + __builtin_amdgcn_logf(l)) * kLn2;
+      }
+    }
   }
 }
 
-// Joins the splits: one group of D / 4 threads per row and head, the
-// partials in split order.  Rows whose sequence was not split are done.
+// Inclusive sum over the wave's lanes (row shifts, then the row totals passed on).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t scan_step(uint32_t v) {
+  return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v = scan_step<0x111, 0xF>(v);                       // row_shr 1, 2, 4, 8
+  v = scan_step<0x112, 0xF>(v);
+  v = scan_step<0x114, 0xF>(v);
+  v = scan_step<0x118, 0xF>(v);
+  v = scan_step<0x142, 0xA>(v);                       // row_bcast 15 into rows 1 and 3
+  return scan_step<0x143, 0xC>(v);                    // row_bcast 31 into rows 2 and 3
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, uint32_t lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, (int)lane);
+}
+
 template <int DT, int D, int QT>
-__global__ __launch_bounds__(256) void kv4_attn_join_kernel(Kv4AttnK a) {
-  constexpr uint32_t RT = 16 * QT, TP = D / 4, kRows = 256 / TP;
-  const uint32_t tid = threadIdx.x, c = tid % TP * 4;
-  const uint64_t id = (uint64_t)blockIdx.x * kRows + tid / TP;
-  const uint64_t row = id / a.hq;
-  const uint32_t hd = (uint32_t)(id % a.hq);
-  if (row >= (uint64_t)a.T) return;
-  uint32_t b = (uint32_t)row;
-  if (a.starts != nullptr) {
-    // the last sequence that starts at or before the row
-    uint32_t lo = 0, hi = a.B;
-    if ((int64_t)a.starts[0] > (int64_t)row) return;
-    while (hi - lo > 1) {
-      const uint32_t mid = (lo + hi) / 2;
-      if ((int64_t)a.starts[mid] <= (int64_t)row) lo = mid; else hi = mid;
+__global__ __launch_bounds__(256, waves_per_simd(D, QT)) void kv4_attn_kernel(Kv4AttnK a) {
+  constexpr uint32_t RT = 16 * QT;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  uint32_t* const red = reinterpret_cast<uint32_t*>(smem);
+  uint32_t* const visits = red + 8;
+  uint32_t* const units = visits + a.B + 1;
+  const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), worker = blockIdx.x * 4 + wave;
+  // up to 64 sequences each wave keeps the plan in its lanes, else the block keeps it in LDS
+  const bool in_lanes = a.B <= 64;
+  Seq mine = {0, 0, 0};
+  uint32_t my_visits = 0, my_units = 0, all_visits, all_units;      // (counts before the lane's sequence)
+  if (in_lanes) {
+    uint32_t nu = 0, nv = 0;
+    if (lane < a.B) {
+      mine = load_seq(a, lane);
+      nu = seq_tiles(a, mine, RT) * a.hkv;
+      nv = nu * (seq_pages(a, mine) + kUnitCost);
     }
-    b = lo;
+    const uint32_t xv = wave_scan(nv), xu = wave_scan(nu);
+    my_visits = lane < a.B ? xv - nv : 0xFFFFFFFFu;
+    my_units = lane < a.B ? xu - nu : 0xFFFFFFFFu;
+    all_visits = lane_value(xv, 63);
+    all_units = lane_value(xu, 63);
+  } else {
+    make_plan(a, RT, visits, units, red);
+    all_visits = uniform(visits[a.B]);
+    all_units = uniform(units[a.B]);
   }
-  if (b >= a.B) return;
-  const Seq sq = load_seq(a, b);
-  if (row < sq.start || row >= (uint64_t)sq.start + sq.rows) return;
-  const uint32_t chunk = a.plan[0], slot0 = a.plan[1 + b];
-  const uint32_t splits = seq_splits(seq_pages(a, sq), chunk);
-  if (splits == 1) return;
-  const uint32_t tiles = seq_tiles(a, sq, RT);
-  const uint32_t head = hd / a.group, r = ((uint32_t)row - sq.start) * a.group + hd % a.group;
-  const uint32_t step = tiles * a.hkv;
-  const uint64_t first = slot0 + (uint64_t)head * tiles + r / RT;
-  if (first + (uint64_t)(splits - 1) * step >= a.max_slots) return;
-  float M = -INFINITY;
-  for (uint32_t s = 0; s < splits; ++s) M = __builtin_fmaxf(M, a.stat[((first + (uint64_t)s * step) * RT + r % RT) * 2]);
-  const float mm = M == -INFINITY ? 0.f : M;
-  float l = 0.f;
-  f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  for (uint32_t s = 0; s < splits; ++s) {
-    const uint64_t at = (first + (uint64_t)s * step) * RT + r % RT;
-    const float f = __builtin_amdgcn_exp2f(a.stat[at * 2] - mm);
-    l += a.stat[at * 2 + 1] * f;
-    o += *reinterpret_cast<const f32x4*>(a.part + at * D + c) * f;
+  const uint32_t run = run_length(a, all_visits, all_units);
+  if (blockIdx.x == 0) {                              // for the launch that joins
+    if (in_lanes) {
+      if (wave == 0 && lane < a.B) a.plan[1 + lane] = my_visits;
+    } else {
+      for (uint32_t b = threadIdx.x; b < a.B; b += 256) a.plan[1 + b] = visits[b];
+    }
+    if (threadIdx.x == 0) a.plan[0] = run;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-  const u32x2 v = {pack16<DT>(o[0] * inv, o[1] * inv), pack16<DT>(o[2] * inv, o[3] * inv)};
-  *reinterpret_cast<u32x2*>(a.out + row * a.ldo_bytes + ((uint64_t)hd * D + c) * 2) = v;
-  if (c == 0 && a.lse) a.lse[row * a.hq + hd] = l == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(l)) * kLn2;
+  const uint32_t total = run ? all_visits : all_units;
+  uint32_t pos = run ? worker * run : worker;
+  const uint32_t end = run ? (total - (pos < total ? pos : total) < run ? total : pos + run) : total;
+  while (pos < end) {
+    uint32_t b, u;
+    Seq sq;
+    if (in_lanes) {
+      // the last lane whose count before it is at most pos (lane 0's is 0)
+      const uint32_t before = run ? my_visits : my_units;
+      const uint64_t at = __builtin_amdgcn_ballot_w64(before <= pos) | 1;
+      b = 63 - (uint32_t)__builtin_clzll(at);
+      sq.start = lane_value(mine.start, b);
+      sq.rows = lane_value(mine.rows, b);
+      sq.len = lane_value(mine.len, b);
+      u = pos - lane_value(before, b);
+    } else {
+      const uint32_t* const count = run ? visits : units;
+      b = uniform(find(count, a.B, pos));
+      sq = load_seq(a, b);
+      u = pos - uniform(count[b]);
+    }
+    const uint32_t tiles = seq_tiles(a, sq, RT), pages = seq_pages(a, sq);
+    uint32_t off = 0, seg = pages;
+    if (run) {
+      // a unit is kUnitCost visits and then its pages
+      const uint32_t unit = pages + kUnitCost, in = u % unit;
+      u = u / unit;
+      const uint32_t take = unit - in < end - pos ? unit - in : end - pos;
+      off = in > kUnitCost ? in - kUnitCost : 0;
+      seg = in + take > kUnitCost ? in + take - kUnitCost - off : 0;
+      pos += take;
+      if (seg == 0) break;                            // (the run ends before the unit's first page)
+    } else {
+      pos += a.workers;
+    }
+    // heads vary fastest, and the tiles that see the most pages come first;
+    // of a wave's units one at most began in an earlier run, and one ends in a later
+    const uint32_t head = u % a.hkv, t = u / a.hkv;
+    run_unit<DT, D, QT>(a, sq, b, tiles - 1 - (t < tiles ? t : tiles - 1), head, off, seg, seg == pages,
+                        2 * worker + (off == 0));
+  }
+}
+
+// Joins the partial results of units that several waves shared, in page
+// order.  D / 4 threads hold a row and head; WIDE: the other groups of its
+// block take every so many-th of its partials (few rows, many partials
+// each), else rows of their own.  Every partial's statistics and values are
+// asked for together and joined by a running maximum, so that a row waits for
+// memory once for its place in the plan and once for its partials.
+template <int DT, int D, int QT, bool WIDE>
+__global__ __launch_bounds__(WIDE ? 512 : 256) void kv4_attn_join_kernel(Kv4AttnK a) {
+  constexpr uint32_t RT = 16 * QT, TP = D / 4, G = (WIDE ? 512 : 256) / TP, U = WIDE ? 8 : 4;
+  __shared__ float sm[G], sl[G];
+  __shared__ __attribute__((aligned(16))) f32x4 so[G][TP];
+  const uint32_t tid = threadIdx.x, col = tid % TP, grp = tid / TP;
+  const uint32_t run = a.plan[0];
+  const uint64_t total = (uint64_t)a.T * a.hq, step = (uint64_t)gridDim.x * (WIDE ? 1 : G);
+  for (uint64_t id = WIDE ? blockIdx.x : (uint64_t)blockIdx.x * G + grp; id < total; id += step) {
+    const uint32_t row = (uint32_t)(id / a.hq), hd = (uint32_t)(id % a.hq);
+    uint32_t b = row;
+    if (a.starts != nullptr) {
+      // the last sequence that starts at or before the row
+      uint32_t lo = 0, hi = a.B;
+      if (run == 0 || a.starts[0] > (int64_t)row) continue;
+      while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (a.starts[mid] <= (int64_t)row) lo = mid; else hi = mid;
+      }
+      b = lo;
+    }
+    const Seq sq = load_seq(a, b);
+    const uint32_t before = a.plan[1 + b];
+    if (run == 0 || row < sq.start || row - sq.start >= sq.rows) continue;
+    const uint32_t tiles = seq_tiles(a, sq, RT), pages = seq_pages(a, sq);
+    const uint32_t r = (row - sq.start) * a.group + hd % a.group;
+    const uint32_t first = before + ((tiles - 1 - r / RT) * a.hkv + hd / a.group) * (pages + kUnitCost) + kUnitCost;
+    const uint32_t i0 = first / run, i1 = (first + pages - 1) / run;
+    if (i0 >= i1 || i1 >= a.workers) continue;        // one wave's: done (or row offsets out of order)
+    float M = -INFINITY, l = 0.f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    constexpr uint32_t stride = WIDE ? G : 1;
+    for (uint32_t i = i0 + (WIDE ? grp : 0); i <= i1; i += U * stride) {
+      float pm[U], pl[U];
+      f32x4 po[U];
+#pragma unroll
+      for (uint32_t k = 0; k < U; ++k) {
+        // wave j's partial: its second where the unit's pages begin in it, else its first
+        const uint32_t j = i + k * stride <= i1 ? i + k * stride : i1;
+        const uint64_t at = (uint64_t)(2 * j + (j == i0)) * RT + r % RT;
+        pm[k] = a.stat[at * 2];
+        pl[k] = a.stat[at * 2 + 1];
+        po[k] = *reinterpret_cast<const f32x4*>(a.part + at * D + 4 * col);
+      }
+      float mn = M;
+#pragma unroll
+      for (uint32_t k = 0; k < U; ++k) mn = __builtin_fmaxf(mn, pm[k]);
+      const float mm = mn == -INFINITY ? 0.f : mn, f = __builtin_amdgcn_exp2f(M - mm);
+      M = mn;
+      l *= f;
+      o *= f;
+#pragma unroll
+      for (uint32_t k = 0; k < U; ++k) {
+        if (i + k * stride > i1) continue;
+        const float e = __builtin_amdgcn_exp2f(pm[k] - mm);
+        l += pl[k] * e;
+        o += po[k] * e;
+      }
+    }
+    if constexpr (WIDE) {
+      if (col == 0) { sm[grp] = M; sl[grp] = l; }
+      so[grp][col] = o;
+      __syncthreads();
+      if (grp == 0) {
+        float mn = M;
+#pragma unroll
+        for (uint32_t k = 1; k < G; ++k) mn = __builtin_fmaxf(mn, sm[k]);
+        const float mm = mn == -INFINITY ? 0.f : mn;
+        l = 0.f;
+        o = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (uint32_t k = 0; k < G; ++k) {
+          const float e = __builtin_amdgcn_exp2f(sm[k] - mm);
+          l += sl[k] * e;
+          o += so[k][col] * e;
+        }
+        M = mn;
+      }
+      __syncthreads();
+      if (grp != 0) continue;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 v = {pack16<DT>(o[0] * inv, o[1] * inv), pack16<DT>(o[2] * inv, o[3] * inv)};
+    *reinterpret_cast<u32x2*>(a.out + (uint64_t)row * a.ldo_bytes + ((uint64_t)hd * D + 4 * col) * 2) = v;
+    if (col == 0 && a.lse) a.lse[(uint64_t)row * a.hq + hd] = l == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(l)) * kLn2;
+  }
 }
 
 // ------------------------------------------------------------------- host --
 
-// Blocks of the launch, and the work items that the plan aims at.
-constexpr uint32_t kBlocks = 512, kTarget = 1024;
-constexpr uint32_t kMinChunk = 4;                     // pages: one a wave
+constexpr uint32_t kSimds = 1024;                      // four to each of 256 CUs
+constexpr uint32_t kJoinBlocks = 2048;
+constexpr uint64_t kWideRows = 1024;                  // rows and heads up to this: a block each
 
 // 16-row tiles a wave: as many as an average sequence fills, up to two.
 int row_tiles(int64_t T, int64_t B, int64_t group) {
@@ -604,32 +751,33 @@ int row_tiles(int64_t T, int64_t B, int64_t group) {
   return rows <= 16 ? 1 : 2;
 }
 
-// No more slots than this hold partials: items of a split sequence take at
-// least half a chunk each, and a chunk is at least 1 / kTarget of the work.
-int64_t most_slots(int64_t T, int64_t B, int64_t max_pages, int64_t hkv, int64_t group, int qt) {
-  const int64_t rt = 16 * qt;
-  // row tiles of all sequences, at most; each at most max_pages chunks of one
-  const __int128 tiles = ((__int128)T * group) / rt + (B < T ? B : T);
-  const __int128 all = tiles * hkv * (max_pages / kMinChunk + 1);
-  const int64_t cap = 2 * kTarget;
-  return all < cap ? (int64_t)all : cap;
+// The waves that can have work, four a block: page visits of all sequences,
+// each as long as its table (the sizes have been bounded).
+uint32_t workers_for(int64_t T, int64_t B, int64_t max_pages, int64_t hkv, int64_t group, int d, int qt) {
+  const int64_t tiles = T * group / (16 * qt) + (B < T ? B : T);
+  const int64_t most = (tiles * hkv * ((max_pages > 0 ? max_pages : 1) + kUnitCost) / kMinRun + 4) & ~(int64_t)3;
+  const int64_t cap = (int64_t)kSimds * waves_per_simd(d, qt);
+  return (uint32_t)(most < cap ? most : cap);
 }
 
 int64_t plan_bytes(int64_t B) { return ((B + 2) * 4 + 255) & ~(int64_t)255; }
 
 template <int DT, int D, int QT>
 hipError_t launch(const Kv4AttnK& k, hipStream_t s) {
-  constexpr uint32_t RT = 16 * QT;
-  const int lds = (int)((8 * RT + RT * (D + 4) + 8 + 2 * (k.B + 1)) * 4);
+  const int lds = (8 + 2 * ((int)k.B + 1)) * 4;
   auto kern = kv4_attn_kernel<DT, D, QT>;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(kBlocks), dim3(256), lds, s, k);
-  e = hipGetLastError();
-  if (e != hipSuccess || k.max_pages <= (int64_t)kMinChunk) return e;      // (nothing can be split)
-  constexpr uint32_t kRows = 256 / (D / 4);
-  const uint64_t blocks = ((uint64_t)k.T * k.hq + kRows - 1) / kRows;
-  hipLaunchKernelGGL((kv4_attn_join_kernel<DT, D, QT>), dim3((uint32_t)blocks), dim3(256), 0, s, k);
+  hipLaunchKernelGGL(kern, dim3(k.workers / 4), dim3(256), lds, s, k);
+  const hipError_t e = hipGetLastError();
+  // (a unit of one page is one wave's)
+  if (e != hipSuccess || k.max_pages <= 1) return e;
+  const uint64_t rows = (uint64_t)k.T * k.hq;
+  if (rows <= kWideRows) {
+    hipLaunchKernelGGL((kv4_attn_join_kernel<DT, D, QT, true>), dim3((uint32_t)rows), dim3(512), 0, s, k);
+  } else {
+    const uint64_t blocks = (rows + 1024 / D - 1) / (1024 / D);
+    hipLaunchKernelGGL((kv4_attn_join_kernel<DT, D, QT, false>), dim3(blocks < kJoinBlocks ? (uint32_t)blocks : kJoinBlocks),
+                       dim3(256), 0, s, k);
+  }
   return hipGetLastError();
 }
 
@@ -644,7 +792,7 @@ int64_t kv4_attn_workspace_bytes(int64_t T, int64_t B, int64_t max_pages, int32_
   if (T <= 0 || B <= 0 || hq == 0) return 0;
   const int64_t group = hq / hkv;
   const int qt = row_tiles(T, B, group);
-  const int64_t rows = most_slots(T, B, max_pages, hkv, group, qt) * 16 * qt;
+  const int64_t rows = (int64_t)2 * workers_for(T, B, max_pages, hkv, group, head_dim, qt) * 16 * qt;
   return plan_bytes(B) + rows * 8 + rows * head_dim * 4;
 }
 
@@ -652,7 +800,8 @@ hipError_t launch_kv4_attn(const Kv4AttnArgs& a, hipStream_t s) {
   Kv4AttnK k;
   const int64_t group = a.hq / a.hkv;
   const int qt = row_tiles(a.T, a.B, group);
-  const int64_t rows = most_slots(a.T, a.B, a.max_pages, a.hkv, group, qt) * 16 * qt;
+  k.workers = workers_for(a.T, a.B, a.max_pages, a.hkv, group, a.head_dim, qt);
+  const int64_t rows = (int64_t)2 * k.workers * 16 * qt;
   k.q = (const uint8_t*)a.q;
   k.ldq_bytes = (uint64_t)a.ldq * 2;
   k.cache = (const uint8_t*)a.cache;
@@ -673,9 +822,6 @@ hipError_t launch_kv4_attn(const Kv4AttnArgs& a, hipStream_t s) {
   k.group = (uint32_t)group;
   k.window = (uint32_t)a.window;
   k.scale2 = a.scale * kLog2e;
-  k.target = kTarget;
-  k.min_chunk = kMinChunk;
-  k.max_slots = (uint32_t)(rows / (16 * qt));
   uint8_t* w = static_cast<uint8_t*>(a.workspace);
   k.plan = reinterpret_cast<uint32_t*>(w);
   k.stat = reinterpret_cast<float*>(w + plan_bytes(a.B));
