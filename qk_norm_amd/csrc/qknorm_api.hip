@@ -399,7 +399,7 @@ int qknorm_kv_append(const void* qkv, int64_t T, int64_t ld, int32_t hq, int32_t
   if (touched && (qkv == nullptr || slots == nullptr)) return QKNORM_E_NULLPTR;
   if (ld > kMaxPitchBytes / 2) return QKNORM_E_UNSUPPORTED;
   if (!aligned16(qkv) || ld % 8 != 0 || !aligned(slots, 8)) return QKNORM_E_ALIGN;
-  if (T >= kMaxHeadIndex / 4) return QKNORM_E_UNSUPPORTED;
+  if (T >= (INT64_C(1) << 28) || T * hkv >= (INT64_C(1) << 28)) return QKNORM_E_UNSUPPORTED;    // 2^32 threads a launch
   if (!touched) return QKNORM_OK;
   const qknorm::Kv4AppendArgs a{qkv, ld, T, hq, hkv, head_dim, cache, num_pages, page_stride, slots, dtype};
   return finish(qknorm::launch_kv4_append(a, static_cast<hipStream_t>(stream)));
@@ -422,7 +422,7 @@ int qknorm_kv_gather(const void* cache, int64_t num_pages, int64_t page_stride, 
   if (ldk > kMaxPitchBytes / es || ldv > kMaxPitchBytes / es) return QKNORM_E_UNSUPPORTED;
   if (!aligned16(k) || !aligned16(v) || (ldk * es) % 16 != 0 || (ldv * es) % 16 != 0 || !aligned(slots, 8))
     return QKNORM_E_ALIGN;
-  if (T >= kMaxHeadIndex / 4) return QKNORM_E_UNSUPPORTED;
+  if (T >= (INT64_C(1) << 28) || T * hkv >= (INT64_C(1) << 28)) return QKNORM_E_UNSUPPORTED;    // 2^32 threads a launch
   if (!touched) return QKNORM_OK;
   const qknorm::Kv4GatherArgs a{cache, num_pages, page_stride, slots, T, hkv, head_dim, k, ldk, v, ldv, dtype};
   return finish(qknorm::launch_kv4_gather(a, static_cast<hipStream_t>(stream)));

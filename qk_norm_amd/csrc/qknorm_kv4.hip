@@ -48,6 +48,35 @@ __device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
   return v;
 }
 
+// W consecutive dwords (aligned to 4 * W bytes, 16 at most).
+template <int W>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&v)[W]) {
+  if constexpr (W == 2) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+    v[0] = x[0];
+    v[1] = x[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      const u32x4 x = load16(p + 16 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * i + e] = x[e];
+    }
+  }
+}
+template <int W>
+__device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&v)[W]) {
+  if constexpr (W == 2) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    *reinterpret_cast<u32x2*>(p) = u32x2{v[0], v[1]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i)
+      *reinterpret_cast<u32x4*>(p + 16 * i) = u32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+  }
+}
+
 // The code of `slot`'s page and place, or false where it names none.
 __device__ __forceinline__ bool slot_place(int64_t slot, int64_t pages, uint64_t page_stride, uint32_t head,
                                            uint32_t head_bytes, uint64_t* base, uint32_t* tok) {
@@ -57,7 +86,7 @@ __device__ __forceinline__ bool slot_place(int64_t slot, int64_t pages, uint64_t
   return true;
 }
 
-// A block takes TOK rows of one head's K (blockIdx.z 0) or V (1), sixteen
+// A block takes TOK rows of one head's K (`which` 0) or V (1), sixteen
 // threads a head vector, D / 16 values each.  K codes go straight out (D / 2
 // consecutive bytes a token).  V codes pass through LDS, so that the lanes
 // of a wave hold consecutive tokens of one dim pair: rows with consecutive
@@ -65,9 +94,11 @@ __device__ __forceinline__ bool slot_place(int64_t slot, int64_t pages, uint64_t
 template <int DT, int D, int TOK>
 __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4AppendK a) {
   constexpr int E = D / 16, W = E / 2, kRowB = D / 2 + 4;       // values and dwords a thread; LDS pitch
+  constexpr uint32_t kGroups = 256 / TOK, kSteps = (D / 8 + kGroups - 1) / kGroups;
   __shared__ __attribute__((aligned(16))) uint8_t lds[TOK * kRowB];
-  const uint32_t tid = threadIdx.x, part = tid % 16, head = blockIdx.y, which = blockIdx.z;
-  const uint32_t row0 = blockIdx.x * TOK;
+  // the blocks of the same rows follow each other, so that a row's heads are read together
+  const uint32_t tid = threadIdx.x, part = tid % 16, hv = blockIdx.x % (2 * a.hkv);
+  const uint32_t which = hv / a.hkv, head = hv % a.hkv, row0 = blockIdx.x / (2 * a.hkv) * TOK;
   uint32_t v[TOK / 16][W];
   int64_t slot[TOK / 16];
   const uint64_t col = (uint64_t)(a.hq + (which ? a.hkv : 0) + head) * D * 2 + part * E * 2;
@@ -77,9 +108,7 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4AppendK a) {
     slot[i] = -1;
     if (r < a.T) {
       slot[i] = a.slots[r];
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.qkv + (uint64_t)r * a.ld_bytes + col);
-#pragma unroll
-      for (int w = 0; w < W; ++w) v[i][w] = p[w];
+      load_words<W>(a.qkv + (uint64_t)r * a.ld_bytes + col, v[i]);
     } else {
 #pragma unroll
       for (int w = 0; w < W; ++w) v[i][w] = 0;
@@ -158,24 +187,12 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(Kv4AppendK a) {
   if (!slot_place(a.slots[r], a.pages, a.page_stride, head, kv4_head_bytes(D), &base, &tok)) return;
   uint8_t* out = a.cache + base + 32 * D + tok;
 #pragma unroll
-  for (uint32_t d = tid / TOK; d < D / 8; d += 256 / TOK) {
+  for (uint32_t k = 0; k < kSteps; ++k) {
+    const uint32_t d = tid / TOK + k * kGroups;
+    if (kSteps * kGroups > D / 8 && d >= D / 8) break;
     const uint32_t c = *reinterpret_cast<const uint32_t*>(lds + t * kRowB + d * 4);
 #pragma unroll
     for (int e = 0; e < 4; ++e) out[(uint64_t)(d * 4 + e) * kKv4Tokens] = (uint8_t)(c >> (8 * e));
-  }
-}
-
-template <int DT>
-__device__ __forceinline__ void store_pair(uint8_t* p, float a, float b) {
-  if constexpr (DT == kF32) {
-    reinterpret_cast<float*>(p)[0] = a;
-    reinterpret_cast<float*>(p)[1] = b;
-  } else if constexpr (DT == kBF16) {
-    const bf16x2 h = {(__bf16)a, (__bf16)b};
-    *reinterpret_cast<uint32_t*>(p) = __builtin_bit_cast(uint32_t, h);
-  } else {
-    const f16x2 h = {(_Float16)a, (_Float16)b};
-    *reinterpret_cast<uint32_t*>(p) = __builtin_bit_cast(uint32_t, h);
   }
 }
 
@@ -183,43 +200,87 @@ __device__ __forceinline__ void store_pair(uint8_t* p, float a, float b) {
 // The same blocks and threads as the append's; V passes through LDS the other way.
 template <int DT, int D, int TOK>
 __global__ __launch_bounds__(256) void kv4_gather_kernel(Kv4GatherK a) {
-  constexpr int E = D / 16, W = E / 2, kRowB = D / 2 + 4, ES = IoTraits<DT>::kBytes;
+  constexpr int E = D / 16, W = E / 2, kRowB = D / 2 + 4, ES = IoTraits<DT>::kBytes, N = TOK / 16;
+  constexpr uint32_t kGroups = 256 / TOK, kSteps = (D / 8 + kGroups - 1) / kGroups;
   __shared__ __attribute__((aligned(16))) uint8_t lds[TOK * kRowB];
-  const uint32_t tid = threadIdx.x, part = tid % 16, head = blockIdx.y, which = blockIdx.z;
-  const uint32_t row0 = blockIdx.x * TOK;
-  if (which == 1) {
+  // the blocks of the same rows follow each other, so that a row's heads are read together
+  const uint32_t tid = threadIdx.x, part = tid % 16, hv = blockIdx.x % (2 * a.hkv);
+  const uint32_t which = hv / a.hkv, head = hv % a.hkv, row0 = blockIdx.x / (2 * a.hkv) * TOK;
+  if (a.pages == 0) return;
+  // every place first, then every load, so that they are in flight together
+  // (a row without a place reads the cache's first and stores nothing)
+  uint64_t base[N];
+  uint32_t tok[N];
+  bool live[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t r = row0 + i * 16 + tid / 16;
+    base[i] = tok[i] = 0;
+    live[i] = slot_place(r < a.T ? a.slots[r] : -1, a.pages, a.page_stride, head, kv4_head_bytes(D), &base[i], &tok[i]);
+  }
+  uint32_t sbits[N], code[N][(W + 3) / 4];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    sbits[i] = *reinterpret_cast<const uint16_t*>(a.cache + base[i] + 64 * D + which * 128 + tok[i] * 2);
+  auto codes = [&](const uint8_t* c, uint32_t (&out)[(W + 3) / 4]) {
+    if constexpr (E == 4) out[0] = *reinterpret_cast<const uint16_t*>(c);
+    else {
+#pragma unroll
+      for (int d = 0; d < W / 4; ++d) out[d] = reinterpret_cast<const uint32_t*>(c)[d];
+    }
+  };
+  if (which == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) codes(a.cache + base[i] + tok[i] * (D / 2) + part * (E / 2), code[i]);
+  } else {
     const uint32_t t = tid % TOK, r = row0 + t;
-    uint64_t base = 0;
-    uint32_t tok = 0;
-    if (r < a.T && slot_place(a.slots[r], a.pages, a.page_stride, head, kv4_head_bytes(D), &base, &tok)) {
-      const uint8_t* in = a.cache + base + 32 * D + tok;
+    uint64_t vbase = 0;
+    uint32_t vtok = 0;
+    slot_place(r < a.T ? a.slots[r] : -1, a.pages, a.page_stride, head, kv4_head_bytes(D), &vbase, &vtok);
+    const uint8_t* in = a.cache + vbase + 32 * D + vtok;
+    uint32_t c[kSteps];
 #pragma unroll
-      for (uint32_t d = tid / TOK; d < D / 8; d += 256 / TOK) {
-        uint32_t c = 0;
+    for (uint32_t k = 0; k < kSteps; ++k) {
+      const uint32_t d = tid / TOK + k * kGroups;
+      c[k] = 0;
+      if (kSteps * kGroups > D / 8 && d >= D / 8) break;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c |= (uint32_t)in[(uint64_t)(d * 4 + e) * kKv4Tokens] << (8 * e);
-        *reinterpret_cast<uint32_t*>(lds + t * kRowB + d * 4) = c;
-      }
+      for (int e = 0; e < 4; ++e) c[k] |= (uint32_t)in[(uint64_t)(d * 4 + e) * kKv4Tokens] << (8 * e);
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < kSteps; ++k) {
+      const uint32_t d = tid / TOK + k * kGroups;
+      if (kSteps * kGroups > D / 8 && d >= D / 8) break;
+      *reinterpret_cast<uint32_t*>(lds + t * kRowB + d * 4) = c[k];
     }
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) codes(lds + (i * 16 + tid / 16) * kRowB + part * (E / 2), code[i]);
   }
 #pragma unroll
-  for (int i = 0; i < TOK / 16; ++i) {
+  for (int i = 0; i < N; ++i) {
+    if (!live[i]) continue;
     const uint32_t r = row0 + i * 16 + tid / 16;
-    uint64_t base = 0;
-    uint32_t tok = 0;
-    if (r >= a.T || !slot_place(a.slots[r], a.pages, a.page_stride, head, kv4_head_bytes(D), &base, &tok)) continue;
-    const uint8_t* from = which ? lds + (i * 16 + tid / 16) * kRowB : a.cache + base + tok * (D / 2);
-    const float s = __uint_as_float(
-        (uint32_t)*reinterpret_cast<const uint16_t*>(a.cache + base + 64 * D + which * 128 + tok * 2) << 16);
+    const float s = __uint_as_float(sbits[i] << 16);
     uint8_t* out = which ? a.v + (uint64_t)r * a.ldv_bytes : a.k + (uint64_t)r * a.ldk_bytes;
     out += ((uint64_t)head * D + part * E) * ES;
+    uint32_t word[E * ES / 4];
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const uint32_t c = from[part * (E / 2) + w];
-      const f16x2 h = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 0);
-      store_pair<DT>(out + 2 * w * ES, (float)h[0] * s, (float)h[1] * s);
+      const f16x2 h = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(code[i][w / 4] >> (8 * (w % 4)), 1.f, 0);
+      const float x = (float)h[0] * s, y = (float)h[1] * s;
+      if constexpr (DT == kF32) {
+        word[2 * w] = __float_as_uint(x);
+        word[2 * w + 1] = __float_as_uint(y);
+      } else if constexpr (DT == kBF16) {
+        const bf16x2 o = {(__bf16)x, (__bf16)y};
+        word[w] = __builtin_bit_cast(uint32_t, o);
+      } else {
+        const f16x2 o = {(_Float16)x, (_Float16)y};
+        word[w] = __builtin_bit_cast(uint32_t, o);
+      }
     }
+    store_words<E * ES / 4>(out, word);
   }
 }
 
@@ -227,19 +288,19 @@ template <int DT, int D>
 hipError_t append(const Kv4AppendK& k, hipStream_t s) {
   // 16 rows a block while 64 would leave CUs idle; 64 make V's runs of bytes longer
   if (k.T <= 1024) {
-    hipLaunchKernelGGL((kv4_append_kernel<DT, D, 16>), dim3((k.T + 15) / 16, k.hkv, 2), dim3(256), 0, s, k);
+    hipLaunchKernelGGL((kv4_append_kernel<DT, D, 16>), dim3((k.T + 15) / 16 * k.hkv * 2), dim3(256), 0, s, k);
   } else {
-    hipLaunchKernelGGL((kv4_append_kernel<DT, D, 64>), dim3((k.T + 63) / 64, k.hkv, 2), dim3(256), 0, s, k);
+    hipLaunchKernelGGL((kv4_append_kernel<DT, D, 64>), dim3((k.T + 63) / 64 * k.hkv * 2), dim3(256), 0, s, k);
   }
   return hipGetLastError();
 }
 
 template <int DT, int D>
-hipError_t gather(const Kv4GatherK& k, uint32_t hkv, hipStream_t s) {
+hipError_t gather(const Kv4GatherK& k, hipStream_t s) {
   if (k.T <= 1024) {
-    hipLaunchKernelGGL((kv4_gather_kernel<DT, D, 16>), dim3((k.T + 15) / 16, hkv, 2), dim3(256), 0, s, k);
+    hipLaunchKernelGGL((kv4_gather_kernel<DT, D, 16>), dim3((k.T + 15) / 16 * k.hkv * 2), dim3(256), 0, s, k);
   } else {
-    hipLaunchKernelGGL((kv4_gather_kernel<DT, D, 64>), dim3((k.T + 63) / 64, hkv, 2), dim3(256), 0, s, k);
+    hipLaunchKernelGGL((kv4_gather_kernel<DT, D, 64>), dim3((k.T + 63) / 64 * k.hkv * 2), dim3(256), 0, s, k);
   }
   return hipGetLastError();
 }
@@ -278,11 +339,11 @@ hipError_t launch_kv4_gather(const Kv4GatherArgs& a, hipStream_t s) {
   k.ldk_bytes = (uint64_t)a.ldk * es;
   k.ldv_bytes = (uint64_t)a.ldv * es;
   k.T = (uint32_t)a.T;
+  k.hkv = (uint32_t)a.hkv;
   auto pick = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    const uint32_t h = (uint32_t)a.hkv;
-    if (a.dtype == kF32) return gather<kF32, D>(k, h, s);
-    return a.dtype == kF16 ? gather<kF16, D>(k, h, s) : gather<kBF16, D>(k, h, s);
+    if (a.dtype == kF32) return gather<kF32, D>(k, s);
+    return a.dtype == kF16 ? gather<kF16, D>(k, s) : gather<kBF16, D>(k, s);
   };
   if (a.head_dim == 64) return pick(IntC<64>{});
   if (a.head_dim == 128) return pick(IntC<128>{});

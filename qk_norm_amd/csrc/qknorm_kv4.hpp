@@ -33,7 +33,7 @@ struct Kv4GatherK {
   uint8_t* v;
   int64_t pages;
   uint64_t page_stride, ldk_bytes, ldv_bytes;
-  uint32_t T;
+  uint32_t T, hkv;
 };
 
 struct Kv4AttnK {
