@@ -149,9 +149,8 @@ __device__ __forceinline__ DmaOffsets<G> dma_offsets(uint32_t ldx_bytes, uint32_
 // One K step of the block's A and B tiles into a stage, this wave's share.
 // Rows past the end of x or w fall outside their descriptors (the row's own
 // offset already does, whatever the step's) and arrive as zeros.  TAIL: for
-// the one step of K that has only half its columns, `past` pushes the second
-// half of x's rows outside too (its lanes: by the parity of the instruction's
-// rows, which the swizzle turns on), so that whatever w has there meets zeros.
+// the one step of K that is not full, `past` pushes the columns past K of x's
+// rows outside too, so that whatever w has there meets zeros.
 template <class G, bool TAIL = false>
 __device__ __forceinline__ void dma_tile(Rsrc ra, Rsrc rb, const DmaOffsets<G>& o,
                                          uint32_t k_bytes, uint8_t* stage, uint32_t wave,
@@ -164,7 +163,7 @@ __device__ __forceinline__ void dma_tile(Rsrc ra, Rsrc rb, const DmaOffsets<G>& 
     if (j < G::kAInst) {
       const uint32_t R = (wave * G::kAInst + j) * kRows;
       uint32_t va = o.a[j];                      // (locals: the host pass rejects members here)
-      if constexpr (TAIL) va += last ? past[(wave * G::kAInst + j) & 1] : 0u;
+      if constexpr (TAIL) va += last ? past[j] : 0u;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           ra, (__attribute__((address_space(3))) void*)(stage + R * kRowBytes), 16, va, k_bytes,
           0, 0);
@@ -502,17 +501,16 @@ __device__ __forceinline__ void proj_tile(const ProjKArgs& args, uint32_t id, ui
   // first of them only and from the Infinity Cache for the rest.
   const uint32_t shift = QKNORM_PROJ_STAGGER ? uniform(blockIdx.x % 8 * ksteps / 8) : 0;
   const DmaOffsets<G> doff = dma_offsets<G>(ldx_bytes, ldw_bytes, wave, lane);
-  // 8-bit operands may end in half a step: its second half (chunks CPR/2 and
-  // on) of x lies outside (an offset past 2^31 is, whatever is added to it)
-  uint32_t past[2] = {0, 0};
+  // 8-bit operands may end inside a step: its chunks past K of x lie outside
+  // (an offset past 2^31 is, whatever is added to it)
+  uint32_t past[G::kAInst] = {};
   const uint32_t tail_bytes = kInt && K % BK ? (ksteps - 1) * BK * 2 : 0xFFFFFFFFu;
   if constexpr (kInt) {
-    static_assert(G::kInstRows / G::RPB * 2 == G::CPR, "the swizzle's top bit follows the instruction's parity");
     const uint32_t sub = lane / G::CPR, s = lane % G::CPR;
 #pragma unroll
-    for (uint32_t par = 0; par < 2; ++par) {
-      const uint32_t r = par * G::kInstRows + sub;
-      past[par] = (s ^ ((r / G::RPB) % G::CPR)) >= G::CPR / 2 ? 0x80000000u : 0u;
+    for (int j = 0; j < G::kAInst; ++j) {
+      const uint32_t r = (wave * G::kAInst + j) * G::kInstRows + sub;
+      past[j] = (s ^ ((r / G::RPB) % G::CPR)) >= K % BK / 8 ? 0x80000000u : 0u;
     }
   }
   auto dma = [&](uint32_t step, uint8_t* to) {

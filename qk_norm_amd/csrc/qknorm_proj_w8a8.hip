@@ -64,45 +64,70 @@ hipError_t one_shape(const W8a8Args& q, hipStream_t s) {
   return tiles<G, G, DT, D>(q, (T + G::BM - 1) / G::BM * ((N + G::BN - 1) / G::BN), 0, N, s);
 }
 
+// Tile shapes: 64 or 128 rows one head wide (256 columns for head_dim 256),
+// or the 256-row tiles.  The shape is the one whose rounds of the chip's CUs
+// are estimated to take the least time, in units of a round of 64-row tiles;
+// a round of each on a Qwen3-8B layer (hidden 4096): 64 rows 15.2 us, 128
+// rows 19.2, 256 x 128 26.4, 256 x 256 48.5.  By the 16-bit projection's token
+// ranges instead: 11.5 against 9.1 us for 333 tokens by 1728 columns of a
+// hidden size of 2048, 17.0 against 12.8 for 1500 by 2560.
+//
+// What bounds a K step of the smaller tiles is the LDS: 64 rows read 80 KiB
+// of fragments and take in 24 KiB, 830 cycles at 128 bytes a cycle of the 900
+// measured.  Three to six stages, K steps of 256 bytes, and four waves of
+// twice the rows (fewer fragment reads, but one wave a SIMD) measured the
+// same or slower.  The 256 x 256 tiles need the LDS and the matrix cores for
+// 2048 cycles each of the 3300 that a step takes.
+// (head_dim 256: 64 x 256 22.0 us, 128 x 256 26.6, 256 x 256 43.5.)
+constexpr double kCostM = 1.27, kCostH = 1.75;
+constexpr double cost_full(int d) { return d == 256 ? 1.9 : 3.2; }
+
 template <int DT, int D>
 hipError_t by_tokens(const W8a8Args& q, hipStream_t s, int cus) {
   typedef typename std::conditional<D == 256, GeoS256, GeoS>::type S;
   typedef typename std::conditional<D == 256, GeoM256, GeoM>::type M;
   const ProjArgs& a = q.p;
-  if (a.T <= QKNORM_PROJ_SMALL_T) return one_shape<S, DT, D>(q, s);
   const uint32_t T = (uint32_t)a.T, N = (uint32_t)((a.hq + 2 * a.hkv) * D);
-  const uint64_t tiles_m = (uint64_t)((T + M::BM - 1) / M::BM) * ((N + M::BN - 1) / M::BN);
-  if (a.T <= QKNORM_PROJ_MID_T || (a.T <= 2 * QKNORM_PROJ_MID_T && tiles_m <= (uint64_t)(cus > 0 ? cus : 1)))
-    return one_shape<M, DT, D>(q, s);
+  const uint64_t c = cus > 0 ? (uint64_t)cus : 1;
+  auto rounds = [&](uint64_t tiles) { return (double)((tiles + c - 1) / c); };
+  auto count = [&](uint32_t bm, uint32_t bn) { return (uint64_t)((T + bm - 1) / bm) * ((N + bn - 1) / bn); };
   const uint32_t n_split = proj_split_column(T, N, D, cus), m_tiles = (T + kBM - 1) / kBM;
   const uint32_t n_full = m_tiles * ((n_split + kBN - 1) / kBN);
   const uint32_t n_half = n_split < N ? m_tiles * ((N - n_split + GeoH::BN - 1) / GeoH::BN) : 0;
+  const double cost_s = rounds(count(S::BM, S::BN)), cost_m = kCostM * rounds(count(M::BM, M::BN));
+  const double cost_f = cost_full(D) * rounds(n_full) + kCostH * rounds(n_half);
+  if (cost_s <= cost_m && cost_s <= cost_f) return one_shape<S, DT, D>(q, s);
+  if (cost_m <= cost_f) return one_shape<M, DT, D>(q, s);
   return tiles<GeoF, GeoH, DT, D>(q, n_full, n_half, n_split, s);
 }
 
-template <int DT, int D, int KS, int JB, int TB, int PF>
+// The split form: four slices of K by 32 columns for every token count, one,
+// two or four 16-token blocks a weight fragment.  On the Qwen3-8B layer 8.2
+// us at 1 token, 8.7 at 8, 9.9 at 16, 11.4 at 32 and 14.8 at 64 (the 16-bit
+// kernel's slices and columns: 8.2, 9.1, 10.5, 12.1, 14.8; two slices: 8.3,
+// 9.3, 11.1, 13.2, 16.9; 16 columns from 17 tokens: 13.6 and 19.9).  Of the
+// 8.2 us the weight's 25 MB take 4.1 at 6.2 TB/s and the second launch 1.8.
+constexpr int kSlices = 4;
+
+template <int DT, int D, int TB>
 hipError_t split(const W8a8Args& q, void* workspace, hipStream_t s) {
   const uint32_t N = (uint32_t)((q.p.hq + 2 * q.p.hkv) * D);
   const ProjKArgs k = w8a8_args(q);
   float* part = static_cast<float*>(workspace);
-  hipLaunchKernelGGL((qkv_proj_split_kernel<kI8, D, KS, JB, TB, PF>), dim3(N / (16 * JB) * KS), dim3(256), 0, s, k, part);
+  hipLaunchKernelGGL((qkv_proj_split_kernel<kI8, D, kSlices, 2, TB, 4>), dim3(N / 32 * kSlices), dim3(256), 0, s, k, part);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((qkv_proj_split_finish_kernel<kI8, DT, D, KS>), dim3(N / D, (uint32_t)(q.p.T + 15) / 16), dim3(256),
-                     0, s, k, (const float*)part);
+  hipLaunchKernelGGL((qkv_proj_split_finish_kernel<kI8, DT, D, kSlices>), dim3(N / D, (uint32_t)(q.p.T + 15) / 16),
+                     dim3(256), 0, s, k, (const float*)part);
   return hipGetLastError();
 }
 
 template <int DT, int D>
 hipError_t split_by_tokens(const W8a8Args& q, void* w, hipStream_t s) {
-  if (q.p.T <= 8) return split<DT, D, 4, 1, 1, 8>(q, w, s);
-  if (q.p.T <= 16) return split<DT, D, 8, 2, 1, 4>(q, w, s);
-  if (q.p.T <= 32) return split<DT, D, 8, 2, 2, 4>(q, w, s);
-  return split<DT, D, 4, 2, 4, 4>(q, w, s);
+  if (q.p.T <= 16) return split<DT, D, 1>(q, w, s);
+  if (q.p.T <= 32) return split<DT, D, 2>(q, w, s);
+  return split<DT, D, 4>(q, w, s);
 }
-
-// K slices of a token count (as above), for the workspace's size.
-int64_t slices(int64_t T) { return T <= 8 ? 4 : (T <= 32 ? 8 : 4); }
 
 template <template <int, int> class F, class... A>
 hipError_t by_type(const W8a8Args& q, A... args) {
@@ -133,7 +158,7 @@ bool w8a8_shape_ok(const ProjArgs& a) {
 
 int64_t w8a8_workspace_bytes(int64_t T, int64_t N) {
   if (T <= 0 || T > kProjSplitMaxT || N <= 0) return 0;
-  return (slices(T) * T * N * 4 + 255) & ~(int64_t)255;
+  return (kSlices * T * N * 4 + 255) & ~(int64_t)255;
 }
 
 hipError_t launch_w8a8(const W8a8Args& q, void* workspace, hipStream_t s, int cus) {
