@@ -381,7 +381,7 @@ int qknorm_kv_gather(const void *cache, int64_t num_pages, int64_t page_stride, 
  * [0, T]; offsets must not decrease (else the rows concerned are undefined).
  *
  * qkv [T, ld] and out [T, ldo] (hq*head_dim columns used) 16-byte aligned,
- * pitches multiples of 8 elements; other arrays 4-byte aligned; hq a multiple
+ * pitches multiples of 8 elements, ldo at most 32 MiB; other arrays 4-byte aligned; hq a multiple
  * of hkv; scale finite (QKNORM_E_SHAPE); B <= 4096.  out, lse and workspace
  * must not overlap the inputs.  workspace: 16-byte aligned, at least
  * qknorm_kv_attention_workspace_bytes(T, B, max_pages, hq, hkv, head_dim)

@@ -452,7 +452,8 @@ int qknorm_kv_attention(const void* qkv, int64_t T, int64_t ld, const void* cach
   if ((rc = check_cache(cache, num_pages, page_stride, hkv, head_dim, touched))) return rc;
   if (touched && (qkv == nullptr || out == nullptr || seq_lens == nullptr || (max_pages > 0 && page_table == nullptr)))
     return QKNORM_E_NULLPTR;
-  if (ld > kMaxPitchBytes / 2 || ldo > kMaxPitchBytes / 2) return QKNORM_E_UNSUPPORTED;
+  // (a tile's output rows are addressed with 32-bit offsets: pitches at most 32 MiB)
+  if (ld > kMaxPitchBytes / 2 || ldo > kMaxPitchBytes / 4) return QKNORM_E_UNSUPPORTED;
   if (!aligned16(qkv) || !aligned16(out) || ld % 8 != 0 || ldo % 8 != 0) return QKNORM_E_ALIGN;
   if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(q_starts, 4) || !aligned(lse, 4)) return QKNORM_E_ALIGN;
   const int64_t need = qknorm::kv4_attn_workspace_bytes(T, B, max_pages, hq, hkv, head_dim);

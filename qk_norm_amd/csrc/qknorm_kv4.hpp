@@ -49,7 +49,7 @@ struct Kv4AttnK {
   float* part;                 // [slot][row][D]
   int64_t pages, T;
   uint64_t ldq_bytes, ldo_bytes, page_stride, table_stride;
-  uint32_t max_pages, B, hq, hkv, group, window, workers;
+  uint32_t max_pages, B, hq, hkv, group, window, workers, unit_cost;
   float scale2;
 };
 

@@ -82,6 +82,13 @@ CASES = [
     ([300, 640], [1, 1], 4, 2, 128, HF, 64),
     ([300, 70, 1], [5, 20, 1], 7, 1, 64, BF, 33),
     ([2000], [3], 2, 1, 128, BF, 500),
+    # more than 64 rows a sequence on average: the kernel of prompt chunks
+    ([700, 90, 0, 300], [90, 90, 40, 1], 8, 2, 128, BF, 0),
+    ([1000], [200], 4, 2, 64, HF, 100),
+    ([260, 500], [130, 77], 6, 2, 256, BF, 64),
+    ([50], [60], 8, 2, 128, HF, 0),
+    ([129, 64, 1], [129, 64, 1], 3, 1, 64, BF, 0),
+    ([2100], [65], 5, 1, 128, BF, 0),
 ]
 
 
@@ -116,9 +123,11 @@ def test_one_long_sequence_among_short_ones():
 
 
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
-@pytest.mark.parametrize("vscale", [1e-4, 1e3])
+@pytest.mark.parametrize("vscale", [1e-25, 1e-4, 1e3, 1e25])
 def test_values_of_any_magnitude(vscale, dtype):
-    # V's scales far below fp16's range, and far above one
+    # V's scales far below fp16's range, and far above one (an fp16 output holds up to 65504)
+    if dtype == HF and vscale > 1e3:
+        pytest.skip("outputs would be infinite")
     hq, hkv, D, lens = 4, 2, 128, [260, 77]
     print(f"[kv attention] V scales about {vscale}", flush=True)
     rows, cache, table, starts = make(lens, [1, 1], hq, hkv, D, dtype, 21, vscale=vscale)
@@ -163,6 +172,43 @@ def test_hidden_places_may_hold_anything():
     cache[p, :, 64 * D + 2 * 34:64 * D + 2 * 34 + 2] = nan[0:2]
     got, lse = run(rows, cache, table, lens, starts, hq, hkv, D, dtype, window=window)
     assert torch.equal(got[:2], clean[:2]) and bool(got[2:4].isnan().all()) and torch.equal(got[4], clean[4])
+
+
+def test_hidden_places_of_a_prompt_chunk_may_hold_anything():
+    hq, hkv, D, dtype, window = 4, 1, 128, BF, 90
+    lens, new = [200], [100]                                   # row 0 is token 100: sees 11..100; all rows see 110..100
+    rows, cache, table, starts = make(lens, new, hq, hkv, D, dtype, 62)
+    clean, clse = run(rows, cache, table, lens, starts, hq, hkv, D, dtype, window=window)
+    check(clean, clse, rows, cache, table, lens, starts, hq, hkv, D, dtype, window=window)
+    bad = cache.clone()
+    nan = torch.tensor([math.nan, math.inf, -math.inf, 1e38]).to(BF).view(torch.uint8)
+    for t in list(range(200, 256)) + list(range(0, 11)) + [150]:
+        p = int(table[0, t // 64])
+        for at in (64 * D, 64 * D + 128):
+            bad[p, :, at + 2 * (t % 64):at + 2 * (t % 64) + 2] = nan[2 * (t % 4):2 * (t % 4) + 2] if t != 150 else nan[:2]
+    print("[kv attention] hidden places of a chunk", flush=True)
+    got, lse = run(rows, bad, table, lens, starts, hq, hkv, D, dtype, window=window)
+    # token 150 (row 50) is seen by rows 50 .. 99
+    assert torch.equal(got[:50], clean[:50]) and torch.equal(lse[:50], clse[:50])
+    assert bool(got[50:].isnan().all())
+
+
+@pytest.mark.parametrize("vscale", [1e-25, 1e-4, 1e25])
+def test_prompt_chunk_with_values_of_any_magnitude(vscale):
+    hq, hkv, D, dtype, lens = 4, 2, 64, BF, [150]
+    print(f"[kv attention] chunk, V scales about {vscale}", flush=True)
+    rows, cache, table, starts = make(lens, [100], hq, hkv, D, dtype, 63, vscale=vscale)
+    got, lse = run(rows, cache, table, lens, starts, hq, hkv, D, dtype)
+    check(got, lse, rows, cache, table, lens, starts, hq, hkv, D, dtype)
+
+
+def test_pages_that_are_not_there_hide_a_prompt_chunks_tokens():
+    hq, hkv, D, dtype, lens = 4, 2, 64, HF, [400, 200]
+    rows, cache, table, starts = make(lens, [150, 80], hq, hkv, D, dtype, 72)
+    table[0, 1], table[0, 4], table[1, :] = -1, cache.shape[0], 2 ** 31 - 1
+    print("[kv attention] chunk, pages that are not there", flush=True)
+    got, lse = run(rows, cache, table, lens, starts, hq, hkv, D, dtype)
+    check(got, lse, rows, cache, table, lens, starts, hq, hkv, D, dtype)
 
 
 def test_pages_that_are_not_there_hide_their_tokens():
