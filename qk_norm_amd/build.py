@@ -21,7 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, "qknorm_api.hip"), os.path.join(CSRC, "qknorm_kernels.hip"),
            os.path.join(CSRC, "qknorm_proj.hip"), os.path.join(CSRC, "qknorm_proj_w8a8.hip"),
            os.path.join(CSRC, "qknorm_quant.hip"), os.path.join(CSRC, "qknorm_kv4.hip"),
-           os.path.join(CSRC, "qknorm_kv4_attn.hip"), os.path.join(CSRC, "qknorm_kv4_attn_rows.hip")]
+           os.path.join(CSRC, "qknorm_kv4_attn.hip")]
 LIB = os.path.join(HERE, "libqknorm.so")
 CEILING_SOURCES = [os.path.join(CSRC, "ceiling_probe.hip")]
 FAST_SOURCE = os.path.join(CSRC, "pyfast.cpp")

@@ -34,11 +34,512 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "qknorm_kv4_attn.hpp"
+#include "qknorm_device.hpp"
+#include "qknorm_kv4.hpp"
+#include "qknorm_launch.hpp"
 
 namespace qknorm {
 
 namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr uint32_t kMinRun = 2;     // page visits a worker takes at least
+constexpr float kLazy = 8.f;        // powers of two a score may exceed the kept maximum by
+constexpr int kLazyV = 4;           // and a V scale the kept exponent
+constexpr float kNoScore = -1e30f;  // the kept maximum before the first visible score
+
+template <int DT>
+struct AttnElem;
+template <>
+struct AttnElem<kBF16> {
+  static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  // eight codes to eight values, in order
+  static __device__ __forceinline__ u32x4 codes(uint32_t w) {
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.f, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.f, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.f, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.f, 3))};
+  }
+};
+template <>
+struct AttnElem<kF16> {
+  static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ u32x4 codes(uint32_t w) {
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.f, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.f, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.f, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.f, 3))};
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if constexpr (DT == kBF16) {
+    const bf16x2 h = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, h);
+  } else {
+    const f16x2 h = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, h);
+  }
+}
+
+// Over the four lanes of a row (l, l ^ 16, l ^ 32, l ^ 48).
+__device__ __forceinline__ float row_max(float v) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __builtin_fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+
+// The kernel's arguments, read again from where the launch put them.  The
+// kernels have many, and what is read before a loop is kept through it: read
+// this way where they are needed, they do not take the loop's scalar registers.
+__device__ __forceinline__ Kv4AttnK launch_args() {
+  typedef const __attribute__((address_space(4))) Kv4AttnK* Ptr;
+  Ptr p = (Ptr)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const Kv4AttnK*)p;
+}
+
+// ------------------------------------------------------------------ plan --
+
+// A sequence as the kernels see it: its rows [start, start + rows) clamped to
+// the T rows there are, its length to the page table's width.
+struct Seq {
+  uint32_t start, rows, len;
+};
+
+__device__ __forceinline__ Seq load_seq(const Kv4AttnK& a, uint32_t b) {
+  Seq s;
+  int64_t st = b, en = (int64_t)b + 1;
+  if (a.starts != nullptr) {
+    st = a.starts[b];
+    en = a.starts[b + 1];
+  }
+  st = st < 0 ? 0 : (st > a.T ? a.T : st);
+  en = en < st ? st : (en > a.T ? a.T : en);
+  const int64_t most = (int64_t)a.max_pages * kKv4Tokens;
+  int64_t n = a.lens[b];
+  n = n < 0 ? 0 : (n > most ? most : n);
+  s.start = (uint32_t)st;
+  s.rows = (uint32_t)(en - st);
+  s.len = a.pages > 0 ? (uint32_t)n : 0;
+  return s;
+}
+
+// Row tiles of a sequence, and the most pages that one of them sees.
+__device__ __forceinline__ uint32_t seq_tiles(const Kv4AttnK& a, const Seq& s, uint32_t rt) {
+  return (uint32_t)(((uint64_t)s.rows * a.group + rt - 1) / rt);
+}
+__device__ __forceinline__ uint32_t seq_pages(const Kv4AttnK& a, const Seq& s) {
+  uint32_t p = (s.len + kKv4Tokens - 1) / kKv4Tokens;
+  if (a.window) {
+    // (a tile's own rows span at most the sequence's)
+    const uint64_t w = ((uint64_t)a.window + s.rows) / kKv4Tokens + 2;
+    if (w < p) p = (uint32_t)w;
+  }
+  return p > 0 ? p : 1;                               // (a tile that sees nothing still gives zeros)
+}
+// Fills visits[0..B] and units[0..B] with the running counts of page visits
+// and of units (a row tile of one head).
+__device__ __forceinline__ void make_plan(const Kv4AttnK& a, uint32_t rt, uint32_t* visits, uint32_t* units,
+                                          uint32_t* red) {
+  const uint32_t tid = threadIdx.x, lane = tid & 63;
+  uint32_t base_v = 0, base_u = 0;
+  for (uint32_t b0 = 0; b0 < a.B; b0 += 256) {
+    const uint32_t b = b0 + tid;
+    uint32_t nv = 0, nu = 0;
+    if (b < a.B) {
+      const Seq s = load_seq(a, b);
+      nu = seq_tiles(a, s, rt) * a.hkv;
+      nv = nu * (seq_pages(a, s) + a.unit_cost);
+    }
+    uint32_t xv = nv, xu = nu;                       // inclusive scan over the wave
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t uv = __shfl_up(xv, o), uu = __shfl_up(xu, o);
+      if (lane >= (uint32_t)o) { xv += uv; xu += uu; }
+    }
+    if (b0 != 0) __syncthreads();
+    if (lane == 63) { red[tid >> 6] = xv; red[4 + (tid >> 6)] = xu; }
+    __syncthreads();
+    uint32_t pv = base_v, pu = base_u;
+    for (uint32_t w = 0; w < (tid >> 6); ++w) { pv += red[w]; pu += red[4 + w]; }
+    if (b < a.B) { visits[b] = pv + xv - nv; units[b] = pu + xu - nu; }
+    base_v += red[0] + red[1] + red[2] + red[3];
+    base_u += red[4] + red[5] + red[6] + red[7];
+  }
+  if (tid == 0) { visits[a.B] = base_v; units[a.B] = base_u; }
+  __syncthreads();
+}
+
+// Page visits a worker takes, or 0 where each unit is one worker's: where
+// there are two units a worker or more.
+__device__ __forceinline__ uint32_t run_length(const Kv4AttnK& a, uint32_t visits, uint32_t units) {
+  if (units >= 2 * a.workers) return 0;
+  const uint32_t per = visits / a.workers + (visits % a.workers != 0);
+  return per > kMinRun ? per : kMinRun;
+}
+
+// The largest b with count[b] <= i (count[0] = 0 <= i < count[B]).
+__device__ __forceinline__ uint32_t find(const uint32_t* count, uint32_t B, uint32_t i) {
+  uint32_t lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (count[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// ----------------------------------------------------------------- softmax --
+
+// A wave's running state over its pages.  With m a row's kept maximum (in
+// powers of two) and 2^e the size of the V scales, weights are taken relative to
+// 2^M, M = m + e: the exponential then makes what the second product wants,
+// exp2(s - M) * sv, of order one whatever V's magnitude, in fp16's range.
+// l sums exp2(s - M).  e stays within +-60, where no fp32 sum can leave its
+// range; V scales beyond that are multiplied by 2^-rem.
+template <int D, int QT>
+struct State {
+  f32x4 acc[QT][D / 32][2];      // O^T: dim pairs 16*jj + 4g + r, low and high dim
+  float M[QT], l[QT];            // of row l%16 (l: this lane's tokens)
+  int size;                      // e + rem (wave-uniform)
+};
+
+__device__ __forceinline__ int kept_exponent(int size) { return size < -60 ? -60 : (size > 60 ? 60 : size); }
+__device__ __forceinline__ float power_of_two(int e) { return __builtin_amdgcn_ldexpf(1.f, e); }
+
+template <int D, int QT>
+__device__ __forceinline__ void clear(State<D, QT>& st) {
+  st.size = -200;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    st.M[t] = kNoScore;
+    st.l[t] = 0.f;
+#pragma unroll
+    for (int jj = 0; jj < D / 32; ++jj) st.acc[t][jj][0] = st.acc[t][jj][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+}
+
+// A page's part in the running maximum and sum, from its scores s (tile j's
+// row 4g + r: token 16g + 4j + r of the page, which begins at token tok0) and
+// its V scales vc, and its weights w for the second product (tokens 8u + r and
+// 8u + 4 + r of the lane's group).  `full`: every row sees all of the page;
+// else what a row [lo, hi) does not see is taken out, whatever it holds.
+template <int D, int QT>
+__device__ __forceinline__ void weigh(f32x4 (&s)[QT][4], float (&vc)[4][4], State<D, QT>& st, bool full, uint32_t g,
+                                      uint32_t tok0, const uint32_t (&lo)[QT], const uint32_t (&hi)[QT],
+                                      u32x4 (&w)[QT][2]) {
+  // bit 4j + r of a row's mask: whether it sees the lane's token 4j + r.  As
+  // bits the 32 answers take two registers, not 32 pairs of scalar ones.
+  uint32_t sees[QT] = {};
+  auto keep = [](uint32_t mask, int k) { return (uint32_t)__builtin_amdgcn_sbfe((int)mask, k, 1); };   // all ones or none
+  if (!full) {
+    uint32_t any = 0;
+    const int first = (int)(tok0 + 16 * g);
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      const int a = (int)lo[t] - first, b = (int)hi[t] - first;
+      const uint32_t below = (1u << (a < 0 ? 0 : (a > 16 ? 16 : a))) - 1, until = (1u << (b < 0 ? 0 : (b > 16 ? 16 : b))) - 1;
+      sees[t] = until & ~below;
+      any |= sees[t];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          const uint32_t k = keep(sees[t], 4 * j + r);
+          s[t][j][r] = __uint_as_float((__float_as_uint(s[t][j][r]) & k) | (0xFF800000u & ~k));
+        }
+        vc[j][r] = __uint_as_float(__float_as_uint(vc[j][r]) & keep(any, 4 * j + r));
+      }
+  }
+  float vmax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) vmax = __builtin_fmaxf(vmax, vc[j][r]);
+  vmax = row_max(vmax);
+  if (!full) {
+    // rows see different tokens, so the largest scale is taken over the wave
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) vmax = __builtin_fmaxf(vmax, __shfl_xor(vmax, o));
+  }
+  const uint32_t vbits = uniform(__float_as_uint(vmax));
+  const int vsize = vbits == 0 ? -200 : (int)(vbits >> 23) - 126;      // vmax < 2^vsize
+  const float e = (float)kept_exponent(st.size);
+  float top[QT];
+  bool grow = false;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    float x = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x = __builtin_fmaxf(x, s[t][j][r]);
+    top[t] = row_max(x);
+    grow = grow || top[t] + e > st.M[t] + kLazy;
+  }
+  if (vsize > st.size + kLazyV || __builtin_amdgcn_ballot_w64(grow) != 0) {
+    const int size = vsize > st.size ? vsize : st.size, en = kept_exponent(size);
+    const float back = power_of_two((st.size - kept_exponent(st.size)) - (size - en));
+    st.size = size;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      const float Mn = __builtin_fmaxf(st.M[t] - e, top[t]) + (float)en;
+      const float f = __builtin_amdgcn_exp2f(st.M[t] - Mn), fa = f * back;
+      st.M[t] = Mn;
+      st.l[t] *= f;
+#pragma unroll
+      for (int jj = 0; jj < D / 32; ++jj)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) st.acc[t][jj][h][r] *= fa;
+    }
+  }
+  if (st.size != kept_exponent(st.size)) {
+    const float f = power_of_two(kept_exponent(st.size) - st.size);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) vc[j][r] *= f;
+  }
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    float l = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float x = __builtin_amdgcn_exp2f(s[t][j][r] - st.M[t]);
+        l += x;
+        s[t][j][r] = x * vc[j][r];
+      }
+    st.l[t] += l;
+  }
+  if (!full) {
+    // (a hidden token's scale may be NaN)
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[t][j][r] = __uint_as_float(__float_as_uint(s[t][j][r]) & keep(sees[t], 4 * j + r));
+  }
+#pragma unroll
+  for (int t = 0; t < QT; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) w[t][u][r] = pack16<kF16>(s[t][2 * u][r], s[t][2 * u + 1][r]);
+}
+
+// The tokens that row r (new token r / group of n, whose last is the cache's
+// token L - 1) sees: [row_lo, row_hi).
+__device__ __forceinline__ uint32_t row_hi(const Kv4AttnK& a, const Seq& sq, uint32_t r) {
+  const int64_t h = (int64_t)sq.len - sq.rows + r / a.group + 1;
+  return (uint32_t)(h < 0 ? 0 : h);
+}
+__device__ __forceinline__ uint32_t row_lo(const Kv4AttnK& a, uint32_t hi) {
+  return a.window && hi > a.window ? hi - a.window : 0u;
+}
+
+// The end of a unit for one wave: rows first .. first + 16*QT - 1 (those
+// before `last`), which are rows `at` and on of the tile; to the output where
+// the unit is whole, else to the slot's RT rows.
+template <int DT, int D, int QT, int RT>
+__device__ __forceinline__ void store_rows(const Seq& sq, State<D, QT>& st, uint32_t head, uint32_t first,
+                                           uint32_t last, uint32_t at, bool whole, uint32_t slot) {
+  const Kv4AttnK a = launch_args();
+  const uint32_t lane = threadIdx.x & 63, m16 = lane % 16, g = lane / 16;
+  // (offsets from the wave's first row: below 2^31, rows being 32 MiB apart at most)
+  const Rsrc ro = make_rsrc(a.out + (uint64_t)(sq.start + first / a.group) * a.ldo_bytes, 0xFFFFFFFFu);
+  const Rsrc rp = make_rsrc(a.part + ((uint64_t)slot * RT + at) * D, 16 * QT * D * 4);
+  const float back = power_of_two(st.size - kept_exponent(st.size));
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const uint32_t r = first + t * 16 + m16;
+    const float l = row_sum(st.l[t]);
+    if (r >= last) continue;
+    const float f = whole ? (l == 0.f ? 0.f : back / l) : back;
+    const uint32_t hd = head * a.group + r % a.group;
+    const uint32_t ro_at = (r / a.group - first / a.group) * (uint32_t)a.ldo_bytes + hd * D * 2;
+#pragma unroll
+    for (int jj = 0; jj < D / 32; ++jj) {
+      // dims 32*jj + 8g .. + 7
+      const f32x4 (&o)[2] = st.acc[t][jj];
+      if (whole) {
+        const u32x4 v = {pack16<DT>(o[0][0] * f, o[1][0] * f), pack16<DT>(o[0][1] * f, o[1][1] * f),
+                         pack16<DT>(o[0][2] * f, o[1][2] * f), pack16<DT>(o[0][3] * f, o[1][3] * f)};
+        __builtin_amdgcn_raw_buffer_store_b128(v, ro, ro_at + g * 16, jj * 64, 0);
+      } else {
+        const f32x4 x = f32x4{o[0][0], o[1][0], o[0][1], o[1][1]} * f, y = f32x4{o[0][2], o[1][2], o[0][3], o[1][3]} * f;
+        const uint32_t to = m16 * D * 4 + g * 32, k = t * 16 * D * 4 + jj * 128;
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), rp, to, k, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), rp, to, k + 16, 0);
+      }
+    }
+    if (g == 0) {
+      if (!whole) {
+        const uint64_t i = (uint64_t)slot * RT + at + t * 16 + m16;
+        a.stat[i * 2] = st.M[t];
+        a.stat[i * 2 + 1] = l;
+      } else if (a.lse) {
+        a.lse[(uint64_t)(sq.start + r / a.group) * a.hq + hd] = l == 0.f ? -INFINITY : (st.M[t] + __builtin_amdgcn_logf(l)) * kLn2;
+      }
+    }
+  }
+}
+
+// A sequence's page numbers, read with scalar loads (uniform addresses): as
+// vector loads, which return in order, the wait for a number would be a wait
+// for every page in flight.
+typedef const __attribute__((address_space(4))) int32_t* PageTable;
+__device__ __forceinline__ PageTable page_table(const Kv4AttnK& a, uint32_t b) {
+  const uint64_t at = (uint64_t)(a.table + (uint64_t)b * a.table_stride);
+  return (PageTable)(((uint64_t)uniform((uint32_t)(at >> 32)) << 32) | uniform((uint32_t)at));
+}
+
+// The Q rows of a wave as the products' second operands, and the tokens that
+// each sees.
+template <int D, int QT>
+__device__ __forceinline__ void load_q(const Kv4AttnK& a, const Seq& sq, uint32_t head, uint32_t first, uint32_t last,
+                                       u32x4 (&qf)[QT][D / 32], uint32_t (&lo)[QT], uint32_t (&hi)[QT]) {
+  const uint32_t lane = threadIdx.x & 63, m16 = lane % 16, g = lane / 16;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    uint32_t r = first + t * 16 + m16;
+    r = r < last ? r : last - 1;                      // rows past the end repeat the last and are not stored
+    const uint8_t* q = a.q + (uint64_t)(sq.start + r / a.group) * a.ldq_bytes +
+                       ((uint64_t)head * a.group + r % a.group) * D * 2 + g * (D / 4) * 2;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) qf[t][i] = load16(q + 16 * i);
+    hi[t] = row_hi(a, sq, r);
+    lo[t] = row_lo(a, hi[t]);
+  }
+}
+
+// Inclusive sum over the wave's lanes (row shifts, then the row totals passed on).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t scan_step(uint32_t v) {
+  return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v = scan_step<0x111, 0xF>(v);                       // row_shr 1, 2, 4, 8
+  v = scan_step<0x112, 0xF>(v);
+  v = scan_step<0x114, 0xF>(v);
+  v = scan_step<0x118, 0xF>(v);
+  v = scan_step<0x142, 0xA>(v);                       // row_bcast 15 into rows 1 and 3
+  return scan_step<0x143, 0xC>(v);                    // row_bcast 31 into rows 2 and 3
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, uint32_t lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, (int)lane);
+}
+
+// Calls f(sequence, its number, row tile, head, first page, pages, whole,
+// slot) for every piece of work of one wave out of a.workers, rt rows a tile;
+// `smem` holds 8 words and the plan's counts.  Block 0 leaves the plan for the
+// launch that joins.
+template <class F>
+__device__ __forceinline__ void walk(uint32_t rt, uint32_t worker, uint32_t* smem, F f) {
+  const Kv4AttnK a = launch_args();
+  uint32_t* const red = smem;
+  uint32_t* const visits = red + 8;
+  uint32_t* const units = visits + a.B + 1;
+  const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  // up to 64 sequences each wave keeps the plan in its lanes, else the block keeps it in LDS
+  const bool in_lanes = a.B <= 64;
+  Seq mine = {0, 0, 0};
+  uint32_t my_visits = 0, my_units = 0, all_visits, all_units;      // (counts before the lane's sequence)
+  if (in_lanes) {
+    uint32_t nu = 0, nv = 0;
+    if (lane < a.B) {
+      mine = load_seq(a, lane);
+      nu = seq_tiles(a, mine, rt) * a.hkv;
+      nv = nu * (seq_pages(a, mine) + a.unit_cost);
+    }
+    const uint32_t xv = wave_scan(nv), xu = wave_scan(nu);
+    my_visits = lane < a.B ? xv - nv : 0xFFFFFFFFu;
+    my_units = lane < a.B ? xu - nu : 0xFFFFFFFFu;
+    all_visits = lane_value(xv, 63);
+    all_units = lane_value(xu, 63);
+  } else {
+    make_plan(a, rt, visits, units, red);
+    all_visits = uniform(visits[a.B]);
+    all_units = uniform(units[a.B]);
+  }
+  const uint32_t run = run_length(a, all_visits, all_units);
+  if (blockIdx.x == 0) {                              // for the launch that joins
+    if (in_lanes) {
+      if (wave == 0 && lane < a.B) a.plan[1 + lane] = my_visits;
+    } else {
+      for (uint32_t b = threadIdx.x; b < a.B; b += 256) a.plan[1 + b] = visits[b];
+    }
+    if (threadIdx.x == 0) a.plan[0] = run;
+  }
+  const uint32_t total = run ? all_visits : all_units;
+  uint32_t pos = run ? worker * run : worker;
+  const uint32_t end = run ? (total - (pos < total ? pos : total) < run ? total : pos + run) : total;
+  while (pos < end) {
+    const Kv4AttnK a = launch_args();
+    const uint32_t* const visits = smem + 8;
+    const uint32_t* const units = visits + a.B + 1;
+    uint32_t b, u;
+    Seq sq;
+    if (a.B <= 64) {
+      // the last lane whose count before it is at most pos (lane 0's is 0)
+      const uint32_t before = run ? my_visits : my_units;
+      const uint64_t at = __builtin_amdgcn_ballot_w64(before <= pos) | 1;
+      b = 63 - (uint32_t)__builtin_clzll(at);
+      sq.start = lane_value(mine.start, b);
+      sq.rows = lane_value(mine.rows, b);
+      sq.len = lane_value(mine.len, b);
+      u = pos - lane_value(before, b);
+    } else {
+      const uint32_t* const count = run ? visits : units;
+      b = uniform(find(count, a.B, pos));
+      sq = load_seq(a, b);
+      u = pos - uniform(count[b]);
+    }
+    const uint32_t tiles = seq_tiles(a, sq, rt), pages = seq_pages(a, sq);
+    uint32_t off = 0, seg = pages;
+    if (run) {
+      // a unit is a.unit_cost visits and then its pages
+      const uint32_t unit = pages + a.unit_cost, in = u % unit;
+      u = u / unit;
+      const uint32_t take = unit - in < end - pos ? unit - in : end - pos;
+      off = in > a.unit_cost ? in - a.unit_cost : 0;
+      seg = in + take > a.unit_cost ? in + take - a.unit_cost - off : 0;
+      pos += take;
+      if (seg == 0) break;                            // (the run ends before the unit's first page)
+    } else {
+      pos += a.workers;
+    }
+    // heads vary fastest, and the tiles that see the most pages come first;
+    // of a wave's units one at most began in an earlier run, and one ends in a later
+    const uint32_t head = u % a.hkv, t = u / a.hkv;
+    f(sq, b, tiles - 1 - (t < tiles ? t : tiles - 1), head, off, seg, seg == pages, 2 * worker + (off == 0));
+  }
+}
+
+// ------------------------------------------------------------- main kernel --
 
 // What the registers of the kernel for D dims and QT row tiles allow, without
 // spills.  More waves hide more of the memory's latency and of the steps
@@ -226,18 +727,121 @@ __global__ __launch_bounds__(256, waves_per_simd(D, QT)) void kv4_attn_kernel(Kv
        });
 }
 
+// Joins the partial results of units that several waves shared, in page
+// order.  D / 4 threads hold a row and head; WIDE: the other groups of its
+// block take every so many-th of its partials (few rows, many partials
+// each), else rows of their own.  Every partial's statistics and values are
+// asked for together and joined by a running maximum, so that a row waits for
+// memory once for its place in the plan and once for its partials.
+template <int DT, int D, int RT_, bool WIDE>
+__global__ __launch_bounds__(256) void kv4_attn_join_kernel(Kv4AttnK a) {
+  constexpr uint32_t RT = RT_, TP = D / 4, G = 256 / TP, U = 8;
+  __shared__ float sm[G], sl[G];
+  __shared__ __attribute__((aligned(16))) f32x4 so[G][TP];
+  const uint32_t tid = threadIdx.x, col = tid % TP, grp = tid / TP;
+  const uint32_t run = a.plan[0];
+  const uint64_t total = (uint64_t)a.T * a.hq, step = (uint64_t)gridDim.x * (WIDE ? 1 : G);
+  for (uint64_t id = WIDE ? blockIdx.x : (uint64_t)blockIdx.x * G + grp; id < total; id += step) {
+    const uint32_t row = (uint32_t)(id / a.hq), hd = (uint32_t)(id % a.hq);
+    uint32_t b = row;
+    if (a.starts != nullptr) {
+      // the last sequence that starts at or before the row
+      uint32_t lo = 0, hi = a.B;
+      if (run == 0 || a.starts[0] > (int64_t)row) continue;
+      while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (a.starts[mid] <= (int64_t)row) lo = mid; else hi = mid;
+      }
+      b = lo;
+    }
+    const Seq sq = load_seq(a, b);
+    const uint32_t before = a.plan[1 + b];
+    if (run == 0 || row < sq.start || row - sq.start >= sq.rows) continue;
+    const uint32_t tiles = seq_tiles(a, sq, RT), pages = seq_pages(a, sq);
+    const uint32_t r = (row - sq.start) * a.group + hd % a.group;
+    const uint32_t first = before + ((tiles - 1 - r / RT) * a.hkv + hd / a.group) * (pages + a.unit_cost) + a.unit_cost;
+    const uint32_t i0 = first / run, i1 = (first + pages - 1) / run;
+    if (i0 >= i1 || i1 >= a.workers) continue;        // one wave's: done (or row offsets out of order)
+    float M = kNoScore, l = 0.f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    constexpr uint32_t stride = WIDE ? G : 1;
+    for (uint32_t i = i0 + (WIDE ? grp : 0); i <= i1; i += U * stride) {
+      float pm[U], pl[U];
+      f32x4 po[U];
+#pragma unroll
+      for (uint32_t k = 0; k < U; ++k) {
+        // wave j's partial: its second where the unit's pages begin in it, else its first
+        const uint32_t j = i + k * stride <= i1 ? i + k * stride : i1;
+        const uint64_t at = (uint64_t)(2 * j + (j == i0)) * RT + r % RT;
+        pm[k] = a.stat[at * 2];
+        pl[k] = a.stat[at * 2 + 1];
+        po[k] = *reinterpret_cast<const f32x4*>(a.part + at * D + 4 * col);
+      }
+      float mn = M;
+#pragma unroll
+      for (uint32_t k = 0; k < U; ++k) mn = __builtin_fmaxf(mn, pm[k]);
+      const float f = __builtin_amdgcn_exp2f(M - mn);
+      M = mn;
+      l *= f;
+      o *= f;
+#pragma unroll
+      for (uint32_t k = 0; k < U; ++k) {
+        if (i + k * stride > i1) continue;
+        const float e = __builtin_amdgcn_exp2f(pm[k] - M);
+        l += pl[k] * e;
+        o += po[k] * e;
+      }
+    }
+    if constexpr (WIDE) {
+      if (col == 0) { sm[grp] = M; sl[grp] = l; }
+      so[grp][col] = o;
+      __syncthreads();
+      if (grp == 0) {
+        float mn = M;
+#pragma unroll
+        for (uint32_t k = 1; k < G; ++k) mn = __builtin_fmaxf(mn, sm[k]);
+        l = 0.f;
+        o = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (uint32_t k = 0; k < G; ++k) {
+          const float e = __builtin_amdgcn_exp2f(sm[k] - mn);
+          l += sl[k] * e;
+          o += so[k][col] * e;
+        }
+        M = mn;
+      }
+      __syncthreads();
+      if (grp != 0) continue;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 v = {pack16<DT>(o[0] * inv, o[1] * inv), pack16<DT>(o[2] * inv, o[3] * inv)};
+    *reinterpret_cast<u32x2*>(a.out + (uint64_t)row * a.ldo_bytes + ((uint64_t)hd * D + 4 * col) * 2) = v;
+    if (col == 0 && a.lse) a.lse[(uint64_t)row * a.hq + hd] = l == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(l)) * kLn2;
+  }
+}
+
 // ------------------------------------------------------------------- host --
 
 constexpr uint32_t kSimds = 1024;                      // four to each of 256 CUs
-constexpr int kMaxLds = 160 * 1024;
-#ifndef UC_R
-#define UC_R 1
-#define UC_2 3
-#endif
-#ifndef QKNORM_ATTN_ROWS
-#define QKNORM_ATTN_ROWS 64
-#endif
+// LDS of walk()'s plan.
+inline int plan_lds(uint32_t B) { return (8 + 2 * ((int)B + 1)) * 4; }
 
+constexpr uint32_t kJoinBlocks = 2048;
+constexpr uint64_t kWideRows = 1024;                  // rows and heads up to this: a block each
+
+template <int DT, int D, int RT>
+hipError_t launch_join(const Kv4AttnK& k, hipStream_t s) {
+  const uint64_t rows = (uint64_t)k.T * k.hq;
+  if (rows <= kWideRows) {
+    hipLaunchKernelGGL((kv4_attn_join_kernel<DT, D, RT, true>), dim3((uint32_t)rows), dim3(256), 0, s, k);
+  } else {
+    const uint64_t blocks = (rows + 1024 / D - 1) / (1024 / D);
+    hipLaunchKernelGGL((kv4_attn_join_kernel<DT, D, RT, false>), dim3(blocks < kJoinBlocks ? (uint32_t)blocks : kJoinBlocks),
+                       dim3(256), 0, s, k);
+  }
+  return hipGetLastError();
+}
 template <int DT, int D, int QT>
 hipError_t launch(const Kv4AttnK& k, hipStream_t s) {
   hipLaunchKernelGGL((kv4_attn_kernel<DT, D, QT>), dim3(k.workers / 4), dim3(256), plan_lds(k.B), s, k);
@@ -247,9 +851,9 @@ hipError_t launch(const Kv4AttnK& k, hipStream_t s) {
   return launch_join<DT, D, 16 * QT>(k, s);
 }
 
-// How a call is run: rows a tile (16 or 32 a wave, or 128 a block), and how
-// many waves or blocks take runs of page visits: as many as the chip holds,
-// fewer where the sequences, each as long as its table, would not fill them.
+// How a call is run: rows a tile, and how many waves take runs of page
+// visits: as many as the chip holds, fewer where the sequences, each as long as
+// its table, would not fill them.
 struct Shape {
   int tile;
   uint32_t workers;
@@ -257,18 +861,13 @@ struct Shape {
 };
 
 Shape shape_of(int64_t T, int64_t B, int64_t max_pages, int64_t hkv, int64_t group, int d) {
-  // what an average sequence fills; the block's tile from more than two waves' rows
-  const int64_t rows = (T * group + B - 1) / B;
+  // One 16-row tile a wave where an average sequence has no more, else two,
+  // which convert a page's codes once for both.  (Four, one wave a SIMD: 265 us against
+  // 176 for four chunks of 512 rows over 4096 tokens.)
   Shape s;
-  if (rows > QKNORM_ATTN_ROWS && kv4_attn_rows_lds(d, B) <= kMaxLds) {
-    s.tile = kv4_attn_rows_tile();
-    s.workers = kv4_attn_rows_workers(d);
-    s.unit_cost = UC_R;
-  } else {
-    s.tile = rows <= 16 ? 16 : 32;
-    s.workers = kSimds * waves_per_simd(d, s.tile / 16);
-    s.unit_cost = s.tile == 16 ? 6 : UC_2;
-  }
+  s.tile = (T * group + B - 1) / B <= 16 ? 16 : 32;
+  s.workers = kSimds * waves_per_simd(d, s.tile / 16);
+  s.unit_cost = s.tile == 16 ? 6 : 3;
   const int64_t tiles = T * group / s.tile + (B < T ? B : T);
   const int64_t most = (tiles * hkv * ((max_pages > 0 ? max_pages : 1) + s.unit_cost) / kMinRun + 4) & ~(int64_t)3;
   if (most < (int64_t)s.workers) s.workers = (uint32_t)most;
@@ -317,7 +916,6 @@ hipError_t launch_kv4_attn(const Kv4AttnArgs& a, hipStream_t s) {
   k.plan = reinterpret_cast<uint32_t*>(w);
   k.stat = reinterpret_cast<float*>(w + plan_bytes(a.B));
   k.part = reinterpret_cast<float*>(w + plan_bytes(a.B) + rows * 8);
-  if (h.tile > 32) return launch_kv4_attn_rows(k, a.head_dim, a.dtype, s);
   auto pick = [&](auto d) {
     constexpr int D = decltype(d)::value;
     if (h.tile == 16) return a.dtype == kF16 ? launch<kF16, D, 1>(k, s) : launch<kBF16, D, 1>(k, s);
