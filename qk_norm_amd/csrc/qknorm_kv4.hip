@@ -73,7 +73,7 @@ __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&v)[W]) 
   } else {
 #pragma unroll
     for (int i = 0; i < W / 4; ++i)
-      *reinterpret_cast<u32x4*>(p + 16 * i) = u32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+      __builtin_nontemporal_store(u32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}, reinterpret_cast<u32x4*>(p + 16 * i));
   }
 }
 
@@ -284,10 +284,13 @@ __global__ __launch_bounds__(256) void kv4_gather_kernel(Kv4GatherK a) {
   }
 }
 
+constexpr uint32_t kFewRows = 4096;
+
 template <int DT, int D>
 hipError_t append(const Kv4AppendK& k, hipStream_t s) {
-  // 16 rows a block while 64 would leave CUs idle; 64 make V's runs of bytes longer
-  if (k.T <= 1024) {
+  // 64 rows a block make V's runs of bytes longer; 16 fill the CUs sooner: 1500
+  // rows of 8 heads in and out 8.0 us against 9.4, 8192 rows 21.9 against 23
+  if (k.T <= kFewRows) {
     hipLaunchKernelGGL((kv4_append_kernel<DT, D, 16>), dim3((k.T + 15) / 16 * k.hkv * 2), dim3(256), 0, s, k);
   } else {
     hipLaunchKernelGGL((kv4_append_kernel<DT, D, 64>), dim3((k.T + 63) / 64 * k.hkv * 2), dim3(256), 0, s, k);
@@ -297,7 +300,7 @@ hipError_t append(const Kv4AppendK& k, hipStream_t s) {
 
 template <int DT, int D>
 hipError_t gather(const Kv4GatherK& k, hipStream_t s) {
-  if (k.T <= 1024) {
+  if (k.T <= kFewRows) {
     hipLaunchKernelGGL((kv4_gather_kernel<DT, D, 16>), dim3((k.T + 15) / 16 * k.hkv * 2), dim3(256), 0, s, k);
   } else {
     hipLaunchKernelGGL((kv4_gather_kernel<DT, D, 64>), dim3((k.T + 63) / 64 * k.hkv * 2), dim3(256), 0, s, k);

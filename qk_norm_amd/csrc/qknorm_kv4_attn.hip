@@ -14,8 +14,8 @@
 // tokens by 16 rows), with tile j's row 4g + r holding token 16g + 4j + r:
 // lane group g then has the 16 tokens 16g .. 16g+15 of its row, which are the
 // weights that the second product, O^T = V^T P, wants of it as its second
-// operand, so the weights never leave their lane.  V codes lie dim pair by dim pair, so
-// a lane's 16 tokens of a pair are one 16-byte load.
+// operand, so the weights never leave their lane.  V codes lie dim pair by dim
+// pair, so a lane's 16 tokens of a pair are one 16-byte load.
 //
 // The weights are rounded to fp16 for that product, in both types: 11 bits
 // against the 8 that a bf16 output keeps.  They stay in fp16's range whatever
@@ -23,14 +23,26 @@
 // more than 8 powers of two.  Statistics and accumulators are fp32.
 //
 // Work is counted in page visits: one page of one head for one tile of rows,
-// and a few more for each tile and head (a unit), for starting and ending it.  The plan is made on the GPU from the lengths there (they
-// may change between replays of a captured graph), the same by every block.
+// and a few more for each tile and head (a unit), for starting and ending it.
+// The plan is made on the GPU from the lengths there (they may change between
+// replays of a captured graph), the same by every block.
 // Where there are few units, all visits laid end to end are cut into equal
 // runs, one a wave, whatever sequences and heads they fall in: a wave
 // then takes the end of one unit's pages, some whole units, and the start of
 // another's, so that it leaves at most two partial results, in the workspace,
 // which a second launch joins in page order.  Where there are many, each is one
-// wave's.  Waves share nothing but the plan.
+// wave's.  Waves share nothing but the plan.  (Runs cut by the pages that each
+// causal tile really sees, instead of taking a sequence's tiles as alike: 202 us
+// against 181 for four chunks of 512 rows over 4096 tokens, since fewer cuts
+// then fall on a unit's end.  A block converting each page into LDS once for
+// 128 rows: 182 us against 176.)
+//
+// What bounds it.  One row tile a sequence: memory.  Four sequences of 131071
+// tokens and 8 KV heads, 554 MB, take 91 us in this kernel, 6.1 TB/s; the
+// vector instructions of a page (366 at head_dim 128) are issued in 46 % of
+// it.  64 sequences of 1024 tokens, 71 MB: 19 us, of which the plan and the
+// first loads take 5.  Two row tiles: vector instructions, 79 % of the time
+// (533 a page of 32 rows, beside 64 matrix products), at 730 TFLOP/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -47,7 +59,6 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr uint32_t kMinRun = 2;     // page visits a worker takes at least
 constexpr float kLazy = 8.f;        // powers of two a score may exceed the kept maximum by
 constexpr int kLazyV = 4;           // and a V scale the kept exponent
 constexpr float kNoScore = -1e30f;  // the kept maximum before the first visible score
@@ -187,12 +198,16 @@ __device__ __forceinline__ void make_plan(const Kv4AttnK& a, uint32_t rt, uint32
   __syncthreads();
 }
 
-// Page visits a worker takes, or 0 where each unit is one worker's: where
-// there are two units a worker or more.
-__device__ __forceinline__ uint32_t run_length(const Kv4AttnK& a, uint32_t visits, uint32_t units) {
+// Page visits a wave takes, or 0 where each unit is one wave's: where there
+// are two units a wave or more.  At least two, and one where the work is
+// single row tiles over up to 40 visits each: then a wave a page and the more
+// partials to join are still faster (a sequence of 1000 tokens 9.3 against 9.9
+// us; of 8192 tokens 15.5 against 13.7, before the join took eight at a time).
+__device__ __forceinline__ uint32_t run_length(const Kv4AttnK& a, uint32_t rt, uint32_t visits, uint32_t units) {
   if (units >= 2 * a.workers) return 0;
   const uint32_t per = visits / a.workers + (visits % a.workers != 0);
-  return per > kMinRun ? per : kMinRun;
+  const uint32_t least = rt == 16 && visits <= 40 * units ? 1 : 2;
+  return per > least ? per : least;
 }
 
 // The largest b with count[b] <= i (count[0] = 0 <= i < count[B]).
@@ -485,7 +500,7 @@ __device__ __forceinline__ void walk(uint32_t rt, uint32_t worker, uint32_t* sme
     all_visits = uniform(visits[a.B]);
     all_units = uniform(units[a.B]);
   }
-  const uint32_t run = run_length(a, all_visits, all_units);
+  const uint32_t run = run_length(a, rt, all_visits, all_units);
   if (blockIdx.x == 0) {                              // for the launch that joins
     if (in_lanes) {
       if (wave == 0 && lane < a.B) a.plan[1 + lane] = my_visits;
@@ -869,7 +884,7 @@ Shape shape_of(int64_t T, int64_t B, int64_t max_pages, int64_t hkv, int64_t gro
   s.workers = kSimds * waves_per_simd(d, s.tile / 16);
   s.unit_cost = s.tile == 16 ? 6 : 3;
   const int64_t tiles = T * group / s.tile + (B < T ? B : T);
-  const int64_t most = (tiles * hkv * ((max_pages > 0 ? max_pages : 1) + s.unit_cost) / kMinRun + 4) & ~(int64_t)3;
+  const int64_t most = (tiles * hkv * ((max_pages > 0 ? max_pages : 1) + s.unit_cost) + 4) & ~(int64_t)3;
   if (most < (int64_t)s.workers) s.workers = (uint32_t)most;
   return s;
 }
