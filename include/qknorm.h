@@ -371,6 +371,8 @@ int qknorm_kv_gather(const void *cache, int64_t num_pages, int64_t page_stride, 
  * only p-window+1..p.  Query head h reads KV head h / (hq/hkv).
  *   out[t,h,:] = sum_j softmax_j(scale * q.K_j) V_j,
  *   lse[t,h]   = log sum_j exp(scale * q.K_j)        (NULL: not wanted)
+ * Scores are fp32 (products beyond its range are infinite); a visible token
+ * whose K, V or Q holds a NaN makes the row NaN, as the formula does.
  * A row that sees no token gets zeros and lse = -infinity.  Rows of no
  * sequence (before q_starts[0], past q_starts[B]) are left as they are.
  * A page number outside [0, num_pages) hides its tokens.  Hidden tokens and
@@ -381,9 +383,10 @@ int qknorm_kv_gather(const void *cache, int64_t num_pages, int64_t page_stride, 
  * [0, T]; offsets must not decrease (else the rows concerned are undefined).
  *
  * qkv [T, ld] and out [T, ldo] (hq*head_dim columns used) 16-byte aligned,
- * pitches multiples of 8 elements, ldo at most 32 MiB; other arrays 4-byte aligned; hq a multiple
- * of hkv; scale finite (QKNORM_E_SHAPE); B <= 4096.  out, lse and workspace
- * must not overlap the inputs.  workspace: 16-byte aligned, at least
+ * pitches multiples of 8 elements, ldo at most 32 MiB; other arrays 4-byte
+ * aligned; hq a multiple of hkv; scale finite (QKNORM_E_SHAPE); B <= 4096.
+ * out, lse and workspace must not overlap the inputs.  workspace: 16-byte
+ * aligned, at least
  * qknorm_kv_attention_workspace_bytes(T, B, max_pages, hq, hkv, head_dim)
  * bytes, contents irrelevant on entry, not shared by calls that can run at the
  * same time (replays of two captured graphs included).

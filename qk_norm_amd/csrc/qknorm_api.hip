@@ -149,8 +149,8 @@ int check_attn(int64_t T, int64_t B, int64_t max_pages, int32_t hq, int32_t hkv,
   if (B > kMaxBatch || T > kMaxRows || T * hq >= kMaxHeadIndex) return QKNORM_E_UNSUPPORTED;
   if (max_pages > (INT64_C(1) << 24)) return QKNORM_E_UNSUPPORTED;
   if ((__int128)T * hq * head_dim >= ((__int128)1 << 34)) return QKNORM_E_UNSUPPORTED;   // threads that join splits
-  // page visits, were every sequence as long as its table: counted in 32 bits
-  if ((__int128)(T * hq / 16 + B * hkv + 1) * (max_pages + 4) >= ((__int128)1 << 31)) return QKNORM_E_UNSUPPORTED;
+  // page visits, were every sequence as long as its table, and a unit's own cost: counted in 32 bits
+  if ((__int128)(T * hq / 16 + B * hkv + 1) * (max_pages + 6) >= ((__int128)1 << 31)) return QKNORM_E_UNSUPPORTED;
   return QKNORM_OK;
 }
 

@@ -325,3 +325,56 @@ def test_heads_that_share_keys_agree():
     got, _ = run(rows, cache, table, [200], starts, hq, hkv, D, BF)
     got = got.view(4, hkv, 4, D)
     assert torch.equal(got, got[:, :, :1].expand_as(got))
+
+
+@pytest.mark.parametrize("D,B,hkv", [(256, 520, 8), (64, 4096, 2), (128, 780, 8)])
+def test_decode_of_more_units_than_waves(D, B, hkv):
+    # lengths 0 .. 90 on two pages a sequence; 520 sequences of 8 heads: each unit is one wave's
+    lens = [(i * 53) % 91 for i in range(B)]
+    print(f"[kv attention] {B} sequences, {hkv} heads, D={D}", flush=True)
+    rows, cache, table, starts = make(lens, [1] * B, hkv, hkv, D, BF, D + B)
+    got, lse = run(rows, cache, table, lens, starts, hkv, hkv, D, BF, decode=True)
+    k = B // 130                                               # (every k-th against the definition)
+    check(got[::k], lse[::k], rows[::k], cache, table[::k], lens[::k], list(range(len(lens[::k]) + 1)), hkv, hkv, D, BF)
+    by_offsets, lse2 = run(rows, cache, table, lens, starts, hkv, hkv, D, BF)
+    assert torch.equal(got, by_offsets) and torch.equal(lse, lse2)
+
+
+def test_prompt_of_more_units_than_waves():
+    # 16 heads of 32-row tiles: 130 tiles over 17 pages
+    hq, hkv, D, n = 64, 16, 256, 1040
+    print("[kv attention] long prompt", flush=True)
+    rows, cache, table, starts = make([n], [n], hq, hkv, D, HF, 17)
+    got, lse = run(rows, cache, table, [n], starts, hq, hkv, D, HF)
+    some = [0, 1, 63, 64, 500, 1039]                           # (each row alone, as the last token of its own prefix)
+    for i in some:
+        lens = [i + 1]
+        o, l, tol, ltol, _ = attention(rows[i:i + 1], cache, table, lens, [0, 1], hq, hkv, D, D ** -0.5, 0, HF)
+        assert bool(((got[i:i + 1].double() - o).abs() <= tol).all()) and bool(((lse[i:i + 1].double() - l).abs() <= ltol).all())
+    assert bool(torch.isfinite(got).all()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("new", [[5, 3], [70, 40]], ids=["few", "many"])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_a_row_of_q_that_is_not_finite_stays_alone(value, new):
+    hq, hkv, D, dtype, lens = 4, 1, 128, BF, [200, 100]
+    rows, cache, table, starts = make(lens, new, hq, hkv, D, dtype, 91)
+    rows[2, 5] = value                                         # row 2, query head 0
+    print(f"[kv attention] {value} in Q", flush=True)
+    got, lse = run(rows, cache, table, lens, starts, hq, hkv, D, dtype)
+    assert bool(got[2, 0].isnan().all()) and bool(lse[2, 0].isnan())
+    rows[2, 5] = 0
+    o, l, tol, ltol, _ = attention(rows, cache, table, lens, starts, hq, hkv, D, D ** -0.5, 0, dtype)
+    rest = torch.ones(rows.shape[0], hq, dtype=torch.bool)
+    rest[2, 0] = False
+    assert bool(((got.double() - o).abs() <= tol)[rest].all()) and bool(((lse.double() - l).abs() <= ltol)[rest].all())
+
+
+def test_row_offsets_out_of_order_touch_nothing_else():
+    # rows of sequences with offsets in order keep their results; run() checks what lies around out and workspace
+    hq, hkv, D, dtype = 4, 2, 64, BF
+    lens = [70, 40, 130, 64]
+    rows, cache, table, _ = make(lens, [2, 2, 2, 2], hq, hkv, D, dtype, 95)
+    print("[kv attention] offsets out of order", flush=True)
+    for starts in ([0, 8, 0, 8, 0], [8, 6, 4, 2, 0], [-3, 100, -7, 50, 2], [2 ** 31 - 1, -2 ** 31, 4, 4, 4]):
+        run(rows, cache, table, lens, starts, hq, hkv, D, dtype)

@@ -150,6 +150,33 @@ def test_past_four_gib():
     assert torch.equal(k.cpu().double(), wk) and torch.equal(v.cpu().double(), wv)
 
 
+@pytest.mark.parametrize("T,hkv,D", [(4100, 2, 64), (4097, 1, 128), (4099, 1, 256)])
+def test_many_rows_at_once(T, hkv, D):
+    # rows of one call against the same rows 500 at a time, for places in order and apart
+    dtype = torch.bfloat16
+    print(f"[kv] {T} rows hkv={hkv} D={D}", flush=True)
+    x = rows(T, 1, hkv, D, dtype, T).cuda()
+    pages = (T + 63) // 64 + 2
+    order = torch.randperm(pages * 64, generator=torch.Generator().manual_seed(D))[:T]
+    for slots in (torch.arange(T) + 37, order):
+        slots = slots.cuda()
+        slots[::97] = -1
+        one = random_cache(pages, hkv, D, 2).cuda()
+        parts = one.clone()
+        q.qknorm_kv_append(x, 1, hkv, D, one, slots)
+        for i in range(0, T, 500):
+            q.qknorm_kv_append(x[i:i + 500], 1, hkv, D, parts, slots[i:i + 500])
+        assert torch.equal(one, parts)
+        got = [torch.full((T, hkv * D), 7.0, dtype=dtype, device="cuda") for _ in range(4)]
+        q.qknorm_kv_gather(one, slots, got[0], got[1], hkv, D)
+        for i in range(0, T, 500):
+            q.qknorm_kv_gather(one, slots[i:i + 500], got[2][i:i + 500], got[3][i:i + 500], hkv, D)
+        torch.cuda.synchronize()
+        for a, b in ((got[0], got[2]), (got[1], got[3])):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+        assert bool((got[0][::97] == 7).all())
+
+
 def test_empty():
     c = torch.zeros(2, 1, 64 * 64 + 256, dtype=torch.uint8, device="cuda")
     none = torch.empty(0, dtype=torch.int64, device="cuda")

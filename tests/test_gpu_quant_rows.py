@@ -83,6 +83,22 @@ def test_pitches_and_many_rows():
     _check(x, _run(x, ldq=1040))
 
 
+def test_past_four_gib():
+    # the last rows of an input whose rows lie 32 MiB apart, and of an output 48 MiB apart
+    T, n = 140, 64
+    wide = torch.empty(T, 1 << 24, dtype=torch.float16, device="cuda")
+    out = torch.empty(T, 48 << 20, dtype=torch.int8, device="cuda")
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn(T, n, generator=g).to(torch.float16)
+    wide[:, :n] = x.cuda()
+    scale = torch.empty(T, device="cuda")
+    print("[quant] past 4 GiB", flush=True)
+    q.qknorm_quant_rows(wide[:, :n], out[:, :n], scale)
+    torch.cuda.synchronize()
+    want, ws = quant_rows(x)
+    assert torch.equal(out[:, :n].cpu(), want) and torch.equal(scale.cpu(), ws)
+
+
 def test_empty():
     q.qknorm_quant_rows(torch.empty(0, 32, dtype=torch.bfloat16, device="cuda"),
                         torch.empty(0, 32, dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda"))
