@@ -5,7 +5,7 @@ the current HIP stream, and every step of the computation runs in the HIP
 kernels of ``libqknorm.so``.  There is no CPU fallback -- if the library is
 not built, or a tensor is not on the GPU, the call raises.
 
-The four entry points keep the C names and semantics (``include/qknorm.h``):
+The entry points keep the C names and semantics (``include/qknorm.h``).  The norms:
 
     qknorm_per_head(qkv, hq, hkv, head_dim, gamma_q, gamma_k, eps)
     qknorm_layerwise(qkv, wq, wk, gamma_q, gamma_k, eps, nshards)
@@ -16,8 +16,17 @@ The four entry points keep the C names and semantics (``include/qknorm.h``):
 float8_e4m3fn with bfloat16 gamma.  It is a [T, ...] tensor whose rows are
 contiguous within themselves
 (``stride(-1) == 1`` and each row packed); its row pitch is ``stride(0)``.
-All calls normalise in place and are enqueued on ``stream`` (default: torch's
-current stream).
+They normalise in place.  Beside them the QKV projection with the norm in its
+epilogue (``qknorm_qkv_proj_per_head`` and its workspace forms), and an
+attention block's low-bit path:
+
+    qknorm_quant_rows(x, q, scale)
+    qknorm_qkv_proj_quant(x, x_scale, w, w_scale, qkv, hq, hkv, head_dim, gamma_q, gamma_k, eps)
+    qknorm_kv_append(qkv, hq, hkv, head_dim, cache, slots)
+    qknorm_kv_gather(cache, slots, k, v, hkv, head_dim)
+    qknorm_kv_attention(qkv, cache, page_table, seq_lens, out, hq, hkv, head_dim)
+
+All calls are enqueued on ``stream`` (default: torch's current stream).
 """
 from __future__ import annotations
 
@@ -491,8 +500,12 @@ def qknorm_qkv_proj_quant(x, x_scale, w, w_scale, qkv, hq: int, hkv: int, head_d
     op, ld = _matrix(qkv, dev, "qkv")
     if x.dtype != torch.int8 or w.dtype != torch.int8:
         raise ValueError("x and w must be int8")
-    if x.shape[0] != qkv.shape[0] or x.shape[1] != w.shape[1] or w.shape[0] != (hq + 2 * hkv) * head_dim:
+    if (x.shape[0] != qkv.shape[0] or x.shape[1] != w.shape[1] or w.shape[0] != (hq + 2 * hkv) * head_dim
+            or qkv.shape[1] < w.shape[0]):
         raise ValueError("x [T, hidden], w [N, hidden] and qkv [T, >= N] do not match")
+    for gamma in () if plain else (gamma_q, gamma_k):
+        if gamma is not None and gamma.numel() != head_dim:
+            raise ValueError("gamma must have head_dim values")
     xs = _vector(x_scale, dev, torch.float32, x.shape[0], "x_scale")
     ws = _vector(w_scale, dev, torch.float32, w.shape[0], "w_scale")
     wsp, nbytes = _workspace(workspace, dev)
@@ -540,7 +553,9 @@ def qknorm_kv_append(qkv, hq: int, hkv: int, head_dim: int, cache, slots, stream
             _raise(rc, "qknorm_kv_append")
         return
     dev = _need_gpu(qkv, "qkv")
-    qp, T, _, ld = _packed_rows(qkv, "qkv")
+    qp, T, width, ld = _packed_rows(qkv, "qkv")
+    if width < (hq + 2 * hkv) * head_dim:
+        raise ValueError("qkv must be [T, >= (hq + 2 * hkv) * head_dim]")
     cp, pages, stride = _cache(cache, dev, hkv, head_dim)
     rc = _on(dev, c.kv_append, qp, T, ld, hq, hkv, head_dim, cp, pages, stride, _slots(slots, dev, T),
              _dtype_code(qkv), _stream(stream, dev))

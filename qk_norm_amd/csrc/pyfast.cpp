@@ -505,6 +505,13 @@ static int space_of(PyObject* o, int64_t* dev, void** ptr, int64_t* bytes) {
   return 1;
 }
 
+/* whether gamma is of no use, None, or n values */
+static int values_or_none(PyObject* o, int unused, int64_t n) {
+  if (unused || o == Py_None) return 1;
+  const at::Tensor* t = tensor_of(o);
+  return t && t->numel() == n;
+}
+
 /* quant_rows_t(x, q, scale, stream) -> int or None */
 static PyObject* f_quant_rows_t(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
@@ -542,7 +549,9 @@ static PyObject* f_qkv_proj_quant_t(PyObject* self, PyObject* const* a, Py_ssize
   const int code = dtype_code(*to), plain = a[11] == Py_True;
   if (code < 0 || (!plain && (!gamma_ptr(a[8], code, dev, &gq) || !gamma_ptr(a[9], code, dev, &gk)))) Py_RETURN_NONE;
   if (as_i32(a[5], &hq) || as_i32(a[6], &hkv) || as_i32(a[7], &d) || as_f32(a[10], &eps)) return NULL;
-  if (N != ((int64_t)hq + 2 * (int64_t)hkv) * d) Py_RETURN_NONE;
+  if (N != ((int64_t)hq + 2 * (int64_t)hkv) * d || wo < N || !values_or_none(a[8], plain, d) ||
+      !values_or_none(a[9], plain, d))
+    Py_RETURN_NONE;
   if (stream_ptr(a[13], dev, &st)) return NULL;
   return PyLong_FromLong(qknorm_qkv_proj_quant(x, ldx, (const float*)xs, w, ldw, (const float*)ws, out, ldo, T, K, hq, hkv, d,
                                                gq, gk, eps, plain ? QKNORM_PROJ_PLAIN : 0, code, work, bytes, st));
@@ -567,7 +576,7 @@ static PyObject* f_kv_append_t(PyObject* self, PyObject* const* a, Py_ssize_t n)
   int32_t hq, hkv, d;
   if (as_i32(a[1], &hq) || as_i32(a[2], &hkv) || as_i32(a[3], &d)) return NULL;
   if (!rows_of(a[0], &dev, &t, &T, &w, &ld, &qkv) || dtype_code(*t) < 0 ||
-      !cache_of(a[4], &dev, hkv, d, &pages, &stride, &cache) ||
+      w < ((int64_t)hq + 2 * (int64_t)hkv) * d || !cache_of(a[4], &dev, hkv, d, &pages, &stride, &cache) ||
       !vector_of(a[5], &dev, c10::ScalarType::Long, T, &slots) || !is_current(dev))
     Py_RETURN_NONE;
   const int code = dtype_code(*t);

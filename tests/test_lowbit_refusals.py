@@ -210,3 +210,27 @@ def test_binding_refuses_wrong_gpu_arguments():
             pytest.fail(f"call {i} was not refused")
     torch.cuda.synchronize()
     assert not out.any() and not cache.any()
+
+
+@pytest.mark.gpu
+def test_binding_refuses_rows_narrower_than_the_heads():
+    # views whose pitch would do, but whose own columns would not; gamma of another length
+    d = dict(device="cuda")
+    wide = torch.zeros(2, 384, dtype=torch.bfloat16, **d)
+    cache = torch.zeros(3, 1, 64 * 64 + 256, dtype=torch.uint8, **d)
+    slots = torch.zeros(2, dtype=torch.int64, **d)
+    x, w, f = torch.zeros(2, 64, dtype=torch.int8, **d), torch.zeros(192, 64, dtype=torch.int8, **d), torch.zeros(192, **d)
+    g = torch.ones(128, dtype=torch.bfloat16, **d)
+    bad = [
+        lambda: q.qknorm_kv_append(wide[:, :128], 1, 1, 64, cache, slots),
+        lambda: q.qknorm_qkv_proj_quant(x, f[:2], w, f, wide[:, :128], 1, 1, 64, plain=True),
+        lambda: q.qknorm_qkv_proj_quant(x, f[:2], w, f, wide, 1, 1, 64, g[:32], g[:64]),
+        lambda: q.qknorm_qkv_proj_quant(x, f[:2], w, f, wide, 1, 1, 64, g[:64], g),
+    ]
+    for i, fn in enumerate(bad):
+        with pytest.raises(ValueError):
+            fn()
+            pytest.fail(f"call {i} was not refused")
+    q.qknorm_qkv_proj_quant(x, f[:2], w, f, wide[:, :192], 1, 1, 64, g[:64], g[:64])
+    torch.cuda.synchronize()
+    assert not wide.any() and not cache.any()
