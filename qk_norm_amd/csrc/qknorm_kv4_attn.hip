@@ -749,13 +749,27 @@ __global__ __launch_bounds__(256, waves_per_simd(D, QT)) void kv4_attn_kernel(Kv
 // each), else rows of their own.  Every partial's statistics and values are
 // asked for together and joined by a running maximum, so that a row waits for
 // memory once for its place in the plan and once for its partials.
+constexpr uint32_t kJoinSeqs = 256;                    // (a thread each)
+
 template <int DT, int D, int RT_, bool WIDE>
 __global__ __launch_bounds__(256) void kv4_attn_join_kernel(Kv4AttnK a) {
   constexpr uint32_t RT = RT_, TP = D / 4, G = 256 / TP, U = 8;
   __shared__ float sm[G], sl[G];
   __shared__ __attribute__((aligned(16))) f32x4 so[G][TP];
   const uint32_t tid = threadIdx.x, col = tid % TP, grp = tid / TP;
+  // where rows are told by offsets: a row's sequence is looked for in LDS, not by
+  // loads that wait for one another
+  __shared__ Seq seqs[kJoinSeqs];
+  __shared__ uint32_t visits[kJoinSeqs];
+  const bool staged = a.starts != nullptr && a.B <= kJoinSeqs;
   const uint32_t run = a.plan[0];
+  if (staged) {
+    if (tid < a.B) {
+      seqs[tid] = load_seq(a, tid);
+      visits[tid] = a.plan[1 + tid];
+    }
+    __syncthreads();
+  }
   const uint64_t total = (uint64_t)a.T * a.hq, step = (uint64_t)gridDim.x * (WIDE ? 1 : G);
   for (uint64_t id = WIDE ? blockIdx.x : (uint64_t)blockIdx.x * G + grp; id < total; id += step) {
     const uint32_t row = (uint32_t)(id / a.hq), hd = (uint32_t)(id % a.hq);
@@ -763,15 +777,16 @@ __global__ __launch_bounds__(256) void kv4_attn_join_kernel(Kv4AttnK a) {
     if (a.starts != nullptr) {
       // the last sequence that starts at or before the row
       uint32_t lo = 0, hi = a.B;
-      if (run == 0 || a.starts[0] > (int64_t)row) continue;
+      if (run == 0) continue;
       while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) / 2;
-        if (a.starts[mid] <= (int64_t)row) lo = mid; else hi = mid;
+        const bool at = staged ? seqs[mid].start <= row : a.starts[mid] <= (int64_t)row;
+        if (at) lo = mid; else hi = mid;
       }
       b = lo;
     }
-    const Seq sq = load_seq(a, b);
-    const uint32_t before = a.plan[1 + b];
+    const Seq sq = staged ? seqs[b] : load_seq(a, b);
+    const uint32_t before = staged ? visits[b] : a.plan[1 + b];
     if (run == 0 || row < sq.start || row - sq.start >= sq.rows) continue;
     const uint32_t tiles = seq_tiles(a, sq, RT), pages = seq_pages(a, sq);
     const uint32_t r = (row - sq.start) * a.group + hd % a.group;
