@@ -35,14 +35,17 @@
 // causal tile really sees, instead of taking a sequence's tiles as alike: 202 us
 // against 181 for four chunks of 512 rows over 4096 tokens, since fewer cuts
 // then fall on a unit's end.  A block converting each page into LDS once for
-// 128 rows: 182 us against 176.)
+// 128 rows: 182 us against 176.  Pages of one row tile through LDS, K two
+// ahead: 102.7 against 102.9 us for four sequences of 131071 tokens, 33.0
+// against 31.6 for a ragged batch of 64.)
 //
 // What bounds it.  One row tile a sequence: memory.  Four sequences of 131071
-// tokens and 8 KV heads, 554 MB, take 91 us in this kernel, 6.1 TB/s; the
-// vector instructions of a page (366 at head_dim 128) are issued in 46 % of
-// it.  64 sequences of 1024 tokens, 71 MB: 19 us, of which the plan and the
-// first loads take 5.  Two row tiles: vector instructions, 79 % of the time
-// (533 a page of 32 rows, beside 64 matrix products), at 730 TFLOP/s.
+// tokens and 8 KV heads, 554 MB, take 91 us in this kernel, 6.1 TB/s, and 87
+// with the softmax and the scores left out.  64 sequences of 1024 tokens, 71 MB:
+// 19 us, of which the plan and the first loads take 5.  Two row tiles: vector
+// instructions, issued in about 70 % of the time (some 500 a page of 32 rows,
+// beside 64 matrix products that take 30 %): four prompts' 512 rows each over
+// 4096 tokens 171 us with the join, 750 TFLOP/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -61,7 +64,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;        // powers of two a score may exceed the kept maximum by
 constexpr int kLazyV = 4;           // and a V scale the kept exponent
-constexpr float kNoScore = -1e30f;  // the kept maximum before the first visible score
+constexpr float kNoScore = -1e30f;  // a partial result's maximum if it has no visible score
 
 template <int DT>
 struct AttnElem;
@@ -102,12 +105,21 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   }
 }
 
+// The larger of two numbers that are no NaN, as the middle one of three with
+// infinity: one instruction, where fmaxf makes operands quiet first if it cannot
+// see where they come from.  (An infinity that the compiler knows, it would
+// turn back into fmaxf: four prompts' 512 rows each 172 against 170 us.)
+__device__ __forceinline__ float max_of(uint32_t a, uint32_t b) {
+  uint32_t top = 0x7F800000u;
+  asm("" : "+s"(top));
+  return __builtin_amdgcn_fmed3f(__uint_as_float(a), __uint_as_float(b), __uint_as_float(top));
+}
 // Over the four lanes of a row (l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float row_max(float v) {
   auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  v = max_of(r[0], r[1]);
   auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __builtin_fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+  return max_of(q[0], q[1]);
 }
 __device__ __forceinline__ float row_sum(float v) {
   auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -226,12 +238,15 @@ __device__ __forceinline__ uint32_t find(const uint32_t* count, uint32_t B, uint
 // powers of two) and 2^e the size of the V scales, weights are taken relative to
 // 2^M, M = m + e: the exponential then makes what the second product wants,
 // exp2(s - M) * sv, of order one whatever V's magnitude, in fp16's range.
-// l sums exp2(s - M).  e stays within +-60, where no fp32 sum can leave its
+// l sums exp2(s - M).  Scores are taken relative to M as they are made (one
+// multiply-add with the K scale), so that the exponential's argument costs
+// nothing more unless M changes.  e stays within +-60, where no fp32 sum can leave its
 // range; V scales beyond that are multiplied by 2^-rem.
 template <int D, int QT>
 struct State {
   f32x4 acc[QT][D / 32][2];      // O^T: dim pairs 16*jj + 4g + r, low and high dim
   float M[QT], l[QT];            // of row l%16 (l: this lane's tokens)
+  float least[QT];               // 0, or -infinity (and M 0) before the row's first visible score
   int size;                      // e + rem (wave-uniform)
 };
 
@@ -243,15 +258,15 @@ __device__ __forceinline__ void clear(State<D, QT>& st) {
   st.size = -200;
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    st.M[t] = kNoScore;
-    st.l[t] = 0.f;
+    st.M[t] = st.l[t] = 0.f;
+    st.least[t] = -INFINITY;
 #pragma unroll
     for (int jj = 0; jj < D / 32; ++jj) st.acc[t][jj][0] = st.acc[t][jj][1] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 }
 
-// A page's part in the running maximum and sum, from its scores s (tile j's
-// row 4g + r: token 16g + 4j + r of the page, which begins at token tok0) and
+// A page's part in the running maximum and sum, from its scores s relative to
+// M (tile j's row 4g + r: token 16g + 4j + r of the page, which begins at token tok0) and
 // its V scales vc, and its weights w for the second product (tokens 8u + r and
 // 8u + 4 + r of the lane's group).  `full`: every row sees all of the page;
 // else what a row [lo, hi) does not see is taken out, whatever it holds.
@@ -309,7 +324,7 @@ __device__ __forceinline__ void weigh(f32x4 (&s)[QT][4], float (&vc)[4][4], Stat
 #pragma unroll
       for (int r = 0; r < 4; ++r) x = __builtin_fmaxf(x, s[t][j][r]);
     top[t] = row_max(x);
-    grow = grow || top[t] + e > st.M[t] + kLazy;
+    grow = grow || top[t] + e > st.least[t] + kLazy;
   }
   if (vsize > st.size + kLazyV || __builtin_amdgcn_ballot_w64(grow) != 0) {
     const int size = vsize > st.size ? vsize : st.size, en = kept_exponent(size);
@@ -317,10 +332,18 @@ __device__ __forceinline__ void weigh(f32x4 (&s)[QT][4], float (&vc)[4][4], Stat
     st.size = size;
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      const float Mn = __builtin_fmaxf(st.M[t] - e, top[t]) + (float)en;
-      const float f = __builtin_amdgcn_exp2f(st.M[t] - Mn), fa = f * back;
-      st.M[t] = Mn;
+      // the new M less the old one; a row without a visible score keeps 0
+      const float to = __builtin_fmaxf(st.least[t] - e, top[t]) + (float)en;
+      const float by = to == -INFINITY ? 0.f : to;
+      // (a row's first: nothing to scale, and 2^-by may be beyond fp32)
+      const float f = __builtin_fminf(__builtin_amdgcn_exp2f(-by), 1.f), fa = f * back;
+      if (top[t] > -INFINITY) st.least[t] = 0.f;
+      st.M[t] += by;
       st.l[t] *= f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[t][j][r] -= by;
 #pragma unroll
       for (int jj = 0; jj < D / 32; ++jj)
 #pragma unroll
@@ -343,7 +366,7 @@ __device__ __forceinline__ void weigh(f32x4 (&s)[QT][4], float (&vc)[4][4], Stat
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float x = __builtin_amdgcn_exp2f(s[t][j][r] - st.M[t]);
+        const float x = __builtin_amdgcn_exp2f(s[t][j][r]);
         l += x;
         s[t][j][r] = x * vc[j][r];
       }
@@ -414,7 +437,7 @@ __device__ __forceinline__ void store_rows(const Seq& sq, State<D, QT>& st, uint
     if (g == 0) {
       if (!whole) {
         const uint64_t i = (uint64_t)slot * RT + at + t * 16 + m16;
-        a.stat[i * 2] = st.M[t];
+        a.stat[i * 2] = st.least[t] == 0.f ? st.M[t] : kNoScore;
         a.stat[i * 2 + 1] = l;
       } else if (a.lse) {
         a.lse[(uint64_t)(sq.start + r / a.group) * a.hq + hd] = l == 0.f ? -INFINITY : (st.M[t] + __builtin_amdgcn_logf(l)) * kLn2;
@@ -616,7 +639,7 @@ __device__ __forceinline__ void load_v(PageV<D>& p, Rsrc page, uint32_t m, uint3
 // Scores of a page (tile j's row 4g + r: token 16g + 4j + r), in powers of two.
 template <int DT, int D, int QT>
 __device__ __forceinline__ void score_page(const PageK<D>& p, const u32x4 (&qf)[QT][D / 32], float scale2,
-                                           f32x4 (&s)[QT][4]) {
+                                           const float (&M)[QT], f32x4 (&s)[QT][4]) {
   constexpr int KD = D / 32;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -637,7 +660,7 @@ __device__ __forceinline__ void score_page(const PageK<D>& p, const u32x4 (&qf)[
       const uint32_t w = p.s[j / 2][2 * (j % 2) + r / 2];
       const float k = __uint_as_float(r % 2 ? w & 0xFFFF0000u : w << 16) * scale2;
 #pragma unroll
-      for (int t = 0; t < QT; ++t) s[t][j][r] *= k;
+      for (int t = 0; t < QT; ++t) s[t][j][r] = __builtin_fmaf(s[t][j][r], k, -M[t]);
     }
 }
 
@@ -711,7 +734,7 @@ __device__ __forceinline__ void run_unit(const Seq& sq, uint32_t b, uint32_t til
       const int32_t after = page_id(pg + 2);
       f32x4 s[QT][4];
       u32x4 w[QT][2];
-      score_page<DT, D, QT>(pk, qf, a.scale2, s);
+      score_page<DT, D, QT>(pk, qf, a.scale2, st.M, s);
       if (more) load_k<D, kPolicy>(pk, nb, m16, g);
       float vc[4][4];
 #pragma unroll
