@@ -31,7 +31,8 @@
 // then takes the end of one unit's pages, some whole units, and the start of
 // another's, so that it leaves at most two partial results, in the workspace,
 // which a second launch joins in page order.  Where there are many, each is one
-// wave's.  Waves share nothing but the plan.  (Runs cut by the pages that each
+// wave's.  Waves share nothing but the plan.  Short sequences take a block a
+// unit instead, whose waves share its pages and join in LDS (block_waves).  (Runs cut by the pages that each
 // causal tile really sees, instead of taking a sequence's tiles as alike: 202 us
 // against 181 for four chunks of 512 rows over 4096 tokens, since fewer cuts
 // then fall on a unit's end.  A block converting each page into LDS once for
@@ -40,7 +41,7 @@
 // against 31.6 for a ragged batch of 64.)
 //
 // What bounds it.  One row tile a sequence: memory.  Four sequences of 131071
-// tokens and 8 KV heads, 554 MB, take 91 us in this kernel, 6.1 TB/s, and 87
+// tokens and 8 KV heads, 554 MB, take 91 us in this kernel, 6.1 TB/s, and 5 less
 // with the softmax and the scores left out.  64 sequences of 1024 tokens, 71 MB:
 // 19 us, of which the plan and the first loads take 5.  Two row tiles: vector
 // instructions, issued in about 70 % of the time (some 500 a page of 32 rows,
@@ -446,6 +447,82 @@ __device__ __forceinline__ void store_rows(const Seq& sq, State<D, QT>& st, uint
   }
 }
 
+// The end of a unit for the W waves of a block: their maxima and sums, then
+// their values 64 dims at a time, through LDS (kJoinBytes); the sums over the
+// waves in their order.
+constexpr int kJoinPitch = 68;                        // floats a row of 64 dims
+template <int QT, int W>
+constexpr int kJoinBytes = (W * 16 * QT * (2 + kJoinPitch) + 16 * QT) * 4;
+
+template <int DT, int D, int QT, int W>
+__device__ __forceinline__ void join_waves(const Seq& sq, State<D, QT>& st, uint32_t head, uint32_t first,
+                                           uint32_t last, float* smem) {
+  constexpr uint32_t R = 16 * QT;
+  const Kv4AttnK a = launch_args();
+  const uint32_t tid = threadIdx.x, lane = tid & 63, m16 = lane % 16, g = lane / 16, wave = uniform(tid >> 6);
+  float* const sm = smem;
+  float* const sl = sm + W * R;
+  float* const sinv = sl + W * R;
+  float* const so = sinv + R;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const float l = row_sum(st.l[t]);
+    if (g == 0) {
+      sm[wave * R + t * 16 + m16] = st.least[t] == 0.f ? st.M[t] : kNoScore;
+      sl[wave * R + t * 16 + m16] = l;
+    }
+  }
+  __syncthreads();
+  const float back = power_of_two(st.size - kept_exponent(st.size));
+  float f[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    float top = sm[t * 16 + m16], l = 0.f;
+#pragma unroll
+    for (int w = 1; w < W; ++w) top = __builtin_fmaxf(top, sm[w * R + t * 16 + m16]);
+#pragma unroll
+    for (int w = 0; w < W; ++w) l += sl[w * R + t * 16 + m16] * __builtin_amdgcn_exp2f(sm[w * R + t * 16 + m16] - top);
+    f[t] = back * __builtin_amdgcn_exp2f((st.least[t] == 0.f ? st.M[t] : kNoScore) - top);
+    const uint32_t r = first + t * 16 + m16;
+    if (wave == 0 && g == 0) {
+      sinv[t * 16 + m16] = l == 0.f ? 0.f : 1.f / l;
+      if (a.lse && r < last)
+        a.lse[(uint64_t)(sq.start + r / a.group) * a.hq + head * a.group + r % a.group] =
+            l == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < D / 64; ++h) {
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // dims 32*jj + 8g .. + 7
+        const f32x4 (&o)[2] = st.acc[t][2 * h + i];
+        float* to = so + (wave * R + t * 16 + m16) * kJoinPitch + 32 * i + 8 * g;
+        *reinterpret_cast<f32x4*>(to) = f32x4{o[0][0], o[1][0], o[0][1], o[1][1]} * f[t];
+        *reinterpret_cast<f32x4*>(to + 4) = f32x4{o[0][2], o[1][2], o[0][3], o[1][3]} * f[t];
+      }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t i = tid; i < R * 32; i += 64 * W) {
+      const uint32_t m = i / 32, r = first + m, d = 2 * (i % 32);
+      if (r >= last) continue;
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        x += so[(w * R + m) * kJoinPitch + d];
+        y += so[(w * R + m) * kJoinPitch + d + 1];
+      }
+      const float inv = sinv[m];
+      *reinterpret_cast<uint32_t*>(a.out + (uint64_t)(sq.start + r / a.group) * a.ldo_bytes +
+                                   ((uint64_t)(head * a.group + r % a.group) * D + 64 * h + d) * 2) =
+          pack16<DT>(x * inv, y * inv);
+    }
+    __syncthreads();
+  }
+}
+
 // A sequence's page numbers, read with scalar loads (uniform addresses): as
 // vector loads, which return in order, the wait for a number would be a wait
 // for every page in flight.
@@ -494,8 +571,9 @@ __device__ __forceinline__ uint32_t lane_value(uint32_t v, uint32_t lane) {
 // Calls f(sequence, its number, row tile, head, first page, pages, whole,
 // slot) for every piece of work of one wave out of a.workers, rt rows a tile;
 // `smem` holds 8 words and the plan's counts.  Block 0 leaves the plan for the
-// launch that joins.
-template <class F>
+// launch that joins.  UNITS: whole units, one after another (a worker is a
+// block then, and every wave of it makes the same calls).
+template <bool UNITS, class F>
 __device__ __forceinline__ void walk(uint32_t rt, uint32_t worker, uint32_t* smem, F f) {
   const Kv4AttnK a = launch_args();
   uint32_t* const red = smem;
@@ -523,8 +601,8 @@ __device__ __forceinline__ void walk(uint32_t rt, uint32_t worker, uint32_t* sme
     all_visits = uniform(visits[a.B]);
     all_units = uniform(units[a.B]);
   }
-  const uint32_t run = run_length(a, rt, all_visits, all_units);
-  if (blockIdx.x == 0) {                              // for the launch that joins
+  const uint32_t run = UNITS ? 0 : run_length(a, rt, all_visits, all_units);
+  if (!UNITS && blockIdx.x == 0) {                              // for the launch that joins
     if (in_lanes) {
       if (wave == 0 && lane < a.B) a.plan[1 + lane] = my_visits;
     } else {
@@ -684,10 +762,11 @@ __device__ __forceinline__ void add_page(const PageV<D>& p, const u32x4 (&w)[QT]
 }
 
 // One unit's pages [off, off + seg): the results where that is all of them,
-// else a partial result in `slot`.
-template <int DT, int D, int QT>
-__device__ __forceinline__ void run_unit(const Seq& sq, uint32_t b, uint32_t tile, uint32_t head,
-                                         uint32_t off, uint32_t seg, bool whole, uint32_t slot) {
+// else a partial result in `slot`.  W > 1: all of its pages, by the W waves of
+// a block, which join their results in `smem`.
+template <int DT, int D, int QT, int W>
+__device__ __forceinline__ void run_unit(const Seq& sq, uint32_t b, uint32_t tile, uint32_t head, uint32_t off,
+                                         uint32_t seg, bool whole, uint32_t slot, float* smem) {
   constexpr uint32_t RT = 16 * QT;
   const Kv4AttnK a = launch_args();
   // One row tile a sequence reads its pages once: streamed (nt), 10 % faster than
@@ -701,8 +780,14 @@ __device__ __forceinline__ void run_unit(const Seq& sq, uint32_t b, uint32_t til
   const uint32_t hi_first = row_hi(a, sq, r0), hi_last = row_hi(a, sq, r1 - 1);
   const uint32_t lo_first = row_lo(a, hi_first), lo_last = row_lo(a, hi_last);
   uint32_t p0 = lo_first / kKv4Tokens, p1 = (hi_last + kKv4Tokens - 1) / kKv4Tokens;
-  p0 += off;
-  p1 = seg < p1 - (p0 < p1 ? p0 : p1) ? p0 + seg : p1;
+  if constexpr (W > 1) {
+    const uint32_t n = p1 > p0 ? p1 - p0 : 0, w = uniform(threadIdx.x >> 6);
+    p1 = p0 + n * (w + 1) / W;
+    p0 += n * w / W;
+  } else {
+    p0 += off;
+    p1 = seg < p1 - (p0 < p1 ? p0 : p1) ? p0 + seg : p1;
+  }
 
   State<D, QT> st;
   clear(st);
@@ -754,16 +839,28 @@ __device__ __forceinline__ void run_unit(const Seq& sq, uint32_t b, uint32_t til
     }
   }
 
-  store_rows<DT, D, QT, RT>(sq, st, head, r0, r1, 0, whole, slot);
+  if constexpr (W > 1)
+    join_waves<DT, D, QT, W>(sq, st, head, r0, r1, smem);
+  else
+    store_rows<DT, D, QT, RT>(sq, st, head, r0, r1, 0, whole, slot);
 }
 
 template <int DT, int D, int QT>
 __global__ __launch_bounds__(256, waves_per_simd(D, QT)) void kv4_attn_kernel(Kv4AttnK) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  walk(16 * QT, blockIdx.x * 4 + uniform(threadIdx.x >> 6), reinterpret_cast<uint32_t*>(smem),
-       [&](const Seq& sq, uint32_t b, uint32_t tile, uint32_t head, uint32_t off, uint32_t seg, bool whole, uint32_t slot) {
-         run_unit<DT, D, QT>(sq, b, tile, head, off, seg, whole, slot);
-       });
+  walk<false>(16 * QT, blockIdx.x * 4 + uniform(threadIdx.x >> 6), reinterpret_cast<uint32_t*>(smem),
+              [&](const Seq& sq, uint32_t b, uint32_t tile, uint32_t head, uint32_t off, uint32_t seg, bool whole,
+                  uint32_t slot) { run_unit<DT, D, QT, 1>(sq, b, tile, head, off, seg, whole, slot, nullptr); });
+}
+
+// Short sequences: a block a unit, its pages shared by W waves, one launch.
+template <int DT, int D, int QT, int W>
+__global__ __launch_bounds__(64 * W, D * QT <= 64 ? 3 : (W > 4 ? 2 : waves_per_simd(D, QT))) void kv4_attn_block_kernel(Kv4AttnK) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  float* const join = reinterpret_cast<float*>(smem);
+  walk<true>(16 * QT, blockIdx.x, reinterpret_cast<uint32_t*>(smem + kJoinBytes<QT, W>),
+             [&](const Seq& sq, uint32_t b, uint32_t tile, uint32_t head, uint32_t off, uint32_t seg, bool whole,
+                 uint32_t slot) { run_unit<DT, D, QT, W>(sq, b, tile, head, off, seg, whole, slot, join); });
 }
 
 // Joins the partial results of units that several waves shared, in page
@@ -899,13 +996,44 @@ hipError_t launch_join(const Kv4AttnK& k, hipStream_t s) {
   }
   return hipGetLastError();
 }
+template <int DT, int D, int QT, int W>
+hipError_t launch_blocks(const Kv4AttnK& k, hipStream_t s) {
+  const int lds = kJoinBytes<QT, W> + plan_lds(k.B);
+  hipLaunchKernelGGL((kv4_attn_block_kernel<DT, D, QT, W>), dim3(k.workers), dim3(64 * W), lds, s, k);
+  return hipGetLastError();
+}
 template <int DT, int D, int QT>
-hipError_t launch(const Kv4AttnK& k, hipStream_t s) {
+hipError_t launch(const Kv4AttnK& k, int block, hipStream_t s) {
+  if (block == 4) return launch_blocks<DT, D, QT, 4>(k, s);
+  if constexpr (QT == 1)
+    if (block == 8) return launch_blocks<DT, D, QT, 8>(k, s);
   hipLaunchKernelGGL((kv4_attn_kernel<DT, D, QT>), dim3(k.workers / 4), dim3(256), plan_lds(k.B), s, k);
   const hipError_t e = hipGetLastError();
   // (a unit of one page is one wave's)
   if (e != hipSuccess || k.max_pages <= 1) return e;
   return launch_join<DT, D, 16 * QT>(k, s);
+}
+
+// Waves of a block a unit, or 0 for equal runs over all waves and a second
+// launch.  Blocks need no second launch and no partial results in memory, but
+// leave waves idle where units are few, or their lengths unlike; so they are
+// taken up to a number of pages (of the longest sequence there could be) that
+// grows with the units (the most there could be).  32 KV-sharing query heads
+// over 8, us by runs / by blocks: one token for one sequence of 1000 tokens 9.2 /
+// 8.5 (2000 tokens: 9.6 / 12.7), for 16 of 1000 13.7 / 9.6, for 64 of 500 19.3 /
+// 11.0, for 64 of up to 2000 19.5 / 19.9, for 64 of up to 8192 31.4 / 62; chunks of
+// 512 rows over 4096 tokens, four: 171 / 162, over up to 5000 81.5 / 66; 256 rows
+// over 4000 39.6 / 31.7; 64 rows over 4000 24.8 / 31.0.  From two units a wave on runs
+// are whole units themselves: eight prompts of 1000 tokens 169 / 188.
+int block_waves(int tile, int64_t units, int64_t pages, int64_t workers) {
+  if (tile == 16) {
+    const int64_t most = units / 10 < 16 ? 16 : (units / 10 > 32 ? 32 : units / 10);
+    if (pages > most) return 0;
+    // (16 of 1000: four waves 10.7; 64 of 500: eight waves 14.4)
+    return pages > 4 && units <= 384 ? 8 : 4;
+  }
+  const int64_t most = units / 4 > 128 ? 128 : units / 4;
+  return pages <= most && units < 2 * workers ? 4 : 0;
 }
 
 // How a call is run: rows a tile, and how many waves take runs of page
@@ -915,9 +1043,11 @@ struct Shape {
   int tile;
   uint32_t workers;
   uint32_t unit_cost;          // page visits that starting and ending a unit counts as
+  int block;                   // or a block of so many waves for each unit (else 0)
+  uint32_t blocks;             // and the most units there can be
 };
 
-Shape shape_of(int64_t T, int64_t B, int64_t max_pages, int64_t hkv, int64_t group, int d) {
+Shape shape_of(int64_t T, int64_t B, int64_t max_pages, int64_t window, int64_t hkv, int64_t group, int d) {
   // One 16-row tile a wave where an average sequence has no more, else two,
   // which convert a page's codes once for both.  (Four, one wave a SIMD: 265 us against
   // 176 for four chunks of 512 rows over 4096 tokens.)
@@ -928,6 +1058,11 @@ Shape shape_of(int64_t T, int64_t B, int64_t max_pages, int64_t hkv, int64_t gro
   const int64_t tiles = T * group / s.tile + (B < T ? B : T);
   const int64_t most = (tiles * hkv * ((max_pages > 0 ? max_pages : 1) + s.unit_cost) + 4) & ~(int64_t)3;
   if (most < (int64_t)s.workers) s.workers = (uint32_t)most;
+  int64_t pages = max_pages;
+  if (window > 0 && (window + T) / kKv4Tokens + 2 < pages) pages = (window + T) / kKv4Tokens + 2;
+  // (up to 64 sequences: the plan is kept in lanes; one page: one wave's anyway)
+  s.blocks = (uint32_t)(tiles * hkv);
+  s.block = pages > 1 && B <= 64 ? block_waves(s.tile, tiles * hkv, pages, kSimds * waves_per_simd(d, s.tile / 16)) : 0;
   return s;
 }
 
@@ -937,7 +1072,8 @@ int64_t plan_bytes(int64_t B) { return ((B + 2) * 4 + 255) & ~(int64_t)255; }
 
 int64_t kv4_attn_workspace_bytes(int64_t T, int64_t B, int64_t max_pages, int32_t hq, int32_t hkv, int32_t head_dim) {
   if (T <= 0 || B <= 0 || hq == 0) return 0;
-  const Shape h = shape_of(T, B, max_pages, hkv, hq / hkv, head_dim);
+  // (the window is not known here: what the form that needs it takes)
+  const Shape h = shape_of(T, B, max_pages, 0, hkv, hq / hkv, head_dim);
   const int64_t rows = (int64_t)2 * h.workers * h.tile;
   return plan_bytes(B) + rows * 8 + rows * head_dim * 4;
 }
@@ -945,8 +1081,8 @@ int64_t kv4_attn_workspace_bytes(int64_t T, int64_t B, int64_t max_pages, int32_
 hipError_t launch_kv4_attn(const Kv4AttnArgs& a, hipStream_t s) {
   Kv4AttnK k;
   const int64_t group = a.hq / a.hkv;
-  const Shape h = shape_of(a.T, a.B, a.max_pages, a.hkv, group, a.head_dim);
-  k.workers = h.workers;
+  const Shape h = shape_of(a.T, a.B, a.max_pages, a.window, a.hkv, group, a.head_dim);
+  k.workers = h.block ? h.blocks : h.workers;
   k.unit_cost = h.unit_cost;
   const int64_t rows = (int64_t)2 * h.workers * h.tile;
   k.q = (const uint8_t*)a.q;
@@ -975,8 +1111,8 @@ hipError_t launch_kv4_attn(const Kv4AttnArgs& a, hipStream_t s) {
   k.part = reinterpret_cast<float*>(w + plan_bytes(a.B) + rows * 8);
   auto pick = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (h.tile == 16) return a.dtype == kF16 ? launch<kF16, D, 1>(k, s) : launch<kBF16, D, 1>(k, s);
-    return a.dtype == kF16 ? launch<kF16, D, 2>(k, s) : launch<kBF16, D, 2>(k, s);
+    if (h.tile == 16) return a.dtype == kF16 ? launch<kF16, D, 1>(k, h.block, s) : launch<kBF16, D, 1>(k, h.block, s);
+    return a.dtype == kF16 ? launch<kF16, D, 2>(k, h.block, s) : launch<kBF16, D, 2>(k, h.block, s);
   };
   if (a.head_dim == 64) return pick(IntC<64>{});
   if (a.head_dim == 128) return pick(IntC<128>{});

@@ -378,3 +378,47 @@ def test_row_offsets_out_of_order_touch_nothing_else():
     print("[kv attention] offsets out of order", flush=True)
     for starts in ([0, 8, 0, 8, 0], [8, 6, 4, 2, 0], [-3, 100, -7, 50, 2], [2 ** 31 - 1, -2 ** 31, 4, 4, 4]):
         run(rows, cache, table, lens, starts, hq, hkv, D, dtype)
+
+
+# Page tables much wider than the sequences need: those calls split units over waves that know nothing of one
+# another, where the ones above mostly give each to a block.
+WIDE = ([(test_against_definition, (i,)) for i in range(len(CASES))]
+        + [(test_values_of_any_magnitude, a) for a in ((1e-25, BF), (1e25, BF), (1e3, HF))]
+        + [(test_scores_that_grow_along_the_cache, (a,)) for a in (1.0, -0.3)]
+        + [(test_prompt_chunk_with_values_of_any_magnitude, (a,)) for a in (1e-25, 1e25)]
+        + [(test_a_row_of_q_that_is_not_finite_stays_alone, a) for a in ((math.nan, [5, 3]), (math.inf, [70, 40]))]
+        + [(f, ()) for f in (test_hidden_places_may_hold_anything, test_hidden_places_of_a_prompt_chunk_may_hold_anything,
+                             test_pages_that_are_not_there_hide_a_prompt_chunks_tokens,
+                             test_pages_that_are_not_there_hide_their_tokens,
+                             test_row_offsets_out_of_order_touch_nothing_else, test_heads_that_share_keys_agree)])
+
+
+@pytest.mark.parametrize("which", range(len(WIDE)))
+def test_wide_page_tables(which, monkeypatch):
+    plain = make
+
+    def wide(*args, **kw):
+        rows, cache, table, starts = plain(*args, **kw)
+        more = torch.full((table.shape[0], 600), 2 ** 31 - 1, dtype=torch.int32)
+        return rows, cache, torch.cat([table, more], 1), starts
+
+    f, args = WIDE[which]
+    print(f"[kv attention] wide table: {f.__name__} {args}", flush=True)
+    monkeypatch.setitem(globals(), "make", wide)
+    f(*args)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,length,new,hkv", [(1, 130, 1, 1), (1, 900, 1, 2), (50, 300, 1, 8), (6, 600, 9, 3), (3, 520, 150, 2)])
+def test_short_sequences(B, length, new, hkv, D):
+    # four and eight waves a block, one and two row tiles; some sequences of other lengths, one of none
+    lens = [max(0, length - 61 * i) for i in range(B)]
+    rows_of = [min(new, 1 + i) if new > 1 and i else new for i in range(B)]
+    print(f"[kv attention] short B={B} length={length} new={new} hkv={hkv} D={D}", flush=True)
+    dtype = HF if D == 128 else BF
+    hq = 4 * hkv
+    rows, cache, table, starts = make(lens, rows_of, hq, hkv, D, dtype, B + length, tail=1)
+    got, lse = run(rows, cache, table, lens, starts, hq, hkv, D, dtype)
+    check(got, lse, rows, cache, table, lens, starts, hq, hkv, D, dtype)
+    again, _ = run(rows, cache, table, lens, starts, hq, hkv, D, dtype, want_lse=False)
+    assert torch.equal(got, again)
