@@ -400,6 +400,65 @@ def bench_proj(q, torch, dev, steps, warmup, T=4096, hidden=4096, hq=32, hkv=8, 
     return res
 
 
+def bench_low_bit(q, torch, dev, steps, B, length, hidden=4096, hq=32, hkv=8, D=128, layers=12):
+    """A decode step of a Qwen3-8B-sized attention block in 8 and 4 bits: B
+    sequences of `length` tokens, one new token each.  Row quantisation, 8-bit
+    QKV projection with per-head QK-Norm, append to the 4-bit cache and
+    attention over it, the steps going round `layers` weights and caches of
+    their own (300 MB of weights, so that the Infinity Cache does not keep one
+    from step to step).  Times per step from replayed hipGraphs, for the four
+    calls together and for each alone."""
+    N = (hq + 2 * hkv) * D
+    g = torch.Generator(device=dev).manual_seed(95)
+    bf = torch.bfloat16
+    x = torch.randn(B, hidden, generator=g, device=dev).to(bf)
+    one = torch.ones(D, dtype=bf, device=dev)
+    wq = torch.empty(layers, N, hidden, dtype=torch.int8, device=dev)
+    ws = torch.empty(layers, N, device=dev)
+    each = (length + 1 + 63) // 64
+    caches = torch.zeros(layers, B * each, hkv, 64 * D + 256, dtype=torch.uint8, device=dev)
+    table = torch.randperm(B * each, generator=g, device=dev).int().view(B, each)
+    slots = table[:, length // 64].long() * 64 + length % 64
+    lens = torch.full((B,), length + 1, dtype=torch.int32, device=dev)
+    every = (table.long()[:, :, None] * 64 + torch.arange(64, device=dev)).flatten()
+    for i in range(layers):
+        q.qknorm_quant_rows((torch.randn(N, hidden, generator=g, device=dev) * hidden ** -0.5).to(bf), wq[i], ws[i])
+        for part in every.split(65536):
+            q.qknorm_kv_append(torch.randn(len(part), 2 * hkv * D, generator=g, device=dev).to(bf), 0, hkv, D,
+                               caches[i], part)
+    xq = torch.empty(B, hidden, dtype=torch.int8, device=dev)
+    xs = torch.empty(B, device=dev)
+    qkv = torch.empty(B, N, dtype=bf, device=dev)
+    out = torch.empty(B, hq * D, dtype=bf, device=dev)
+    w1 = torch.empty(max(1, q.qknorm_qkv_proj_quant_workspace_bytes(B, hq, hkv, D)), dtype=torch.uint8, device=dev)
+    w2 = torch.empty(q.qknorm_kv_attention_workspace_bytes(B, B, each, hq, hkv, D), dtype=torch.uint8, device=dev)
+
+    calls = {
+        "quant_rows": lambda i, s: q.qknorm_quant_rows(x, xq, xs, stream=s),
+        "qkv_proj_quant": lambda i, s: q.qknorm_qkv_proj_quant(xq, xs, wq[i % layers], ws[i % layers], qkv, hq, hkv, D,
+                                                               one, one, workspace=w1, stream=s),
+        "kv_append": lambda i, s: q.qknorm_kv_append(qkv, hq, hkv, D, caches[i % layers], slots, stream=s),
+        "kv_attention": lambda i, s: q.qknorm_kv_attention(qkv, caches[i % layers], table, lens, out, hq, hkv, D,
+                                                           workspace=w2, stream=s),
+    }
+
+    def step(i, s):
+        for f in calls.values():
+            f(i, s)
+
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    warm_clocks(torch, lambda i: step(i, stream))
+    res = {"B": B, "cached_tokens": length, "hidden": hidden, "hq": hq, "hkv": hkv, "head_dim": D, "layers": layers,
+           "weight_bytes": N * (hidden + 4), "cache_bytes_read": B * hkv * (length + 1) * (D + 4)}
+    res["step_us"] = graph_replay_us(torch, step, steps)
+    for name, f in calls.items():
+        res[name + "_us"] = graph_replay_us(torch, f, steps)
+    log(f"low-bit decode B={B} length={length}: " + ", ".join(f"{k} {v:.1f}" for k, v in res.items() if k.endswith("_us")))
+    del wq, ws, caches, w2
+    torch.cuda.empty_cache()
+    return res
+
+
 def bench_decode(q, torch, dev, reps=200):
     """Decode-sized launches: per-head [T, 48, 128] bf16 for T in {1, 8, 16, 64, 128}
     and layerwise [T, 6144] (Q 4096 + K 1024, 8 shards) for T in {1, 4, 32, 256}.
@@ -757,7 +816,7 @@ def main():
     ap.add_argument("--case", default="headline",
                     choices=["headline", "prefill_layerwise", "prefill_per_head", "fp8_per_head",
                              "fp8_prefill_layerwise", "proj", "proj_tokens", "decode", "sweep", "copy", "stream",
-                             "wide_layerwise"],
+                             "wide_layerwise", "low_bit_decode"],
                     help="single case for profiling runs")
     ap.add_argument("--stream-shape", metavar="U,THREADS,CAP",
                     help="with --case stream: one in-place shape only (CAP in blocks per CU, 0: one trip)")
@@ -822,6 +881,10 @@ def main():
                                     8, outlier_frac=0.01)
         print(json.dumps({"case": "wide_layerwise", **bench_layerwise(q, torch, dev, p, args.steps,
                                                                       args.warmup, "wide [4096, 40960]")}))
+        return
+    if args.case == "low_bit_decode":
+        pts = [bench_low_bit(q, torch, dev, args.steps, B, n) for B, n in ((1, 1000), (1, 32000), (16, 4000), (64, 4000))]
+        print(json.dumps({"case": "low_bit_decode", "points": pts}))
         return
     if args.case == "prefill_layerwise":
         p = synth.prefill_rows(T=32768)

@@ -31,14 +31,15 @@
 // then takes the end of one unit's pages, some whole units, and the start of
 // another's, so that it leaves at most two partial results, in the workspace,
 // which a second launch joins in page order.  Where there are many, each is one
-// wave's.  Waves share nothing but the plan.  Short sequences take a block a
-// unit instead, whose waves share its pages and join in LDS (block_waves).  (Runs cut by the pages that each
-// causal tile really sees, instead of taking a sequence's tiles as alike: 202 us
-// against 181 for four chunks of 512 rows over 4096 tokens, since fewer cuts
-// then fall on a unit's end.  A block converting each page into LDS once for
-// 128 rows: 182 us against 176.  Pages of one row tile through LDS, K two
-// ahead: 102.7 against 102.9 us for four sequences of 131071 tokens, 33.0
-// against 31.6 for a ragged batch of 64.)
+// wave's.  Waves share nothing but the plan.  Short sequences and most prompts
+// take a block a unit instead, whose waves share its pages and join in LDS, in
+// one launch (block_waves).
+// Not kept: runs cut by the pages that each causal tile really sees, instead of
+// taking a sequence's tiles as alike (202 us against 181 for four chunks of 512
+// rows over 4096 tokens, since fewer cuts then fall on a unit's end); a block
+// converting each page into LDS once for 128 rows (182 us against 176); pages of one row tile through LDS, K two
+// ahead (102.7 against 102.9 us for four sequences of 131071 tokens, 33.0
+// against 31.6 for a ragged batch of 64).
 //
 // What bounds it.  One row tile a sequence: memory.  Four sequences of 131071
 // tokens and 8 KV heads, 554 MB, take 91 us in this kernel, 6.1 TB/s, and 5 less
@@ -46,7 +47,7 @@
 // 19 us, of which the plan and the first loads take 5.  Two row tiles: vector
 // instructions, issued in about 70 % of the time (some 500 a page of 32 rows,
 // beside 64 matrix products that take 30 %): four prompts' 512 rows each over
-// 4096 tokens 171 us with the join, 750 TFLOP/s.
+// 4096 tokens 171 us in runs with their join, 161 in blocks, 800 TFLOP/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
