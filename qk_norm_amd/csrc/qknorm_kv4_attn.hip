@@ -403,7 +403,10 @@ __device__ __forceinline__ uint32_t row_lo(const Kv4AttnK& a, uint32_t hi) {
 
 // The end of a unit for one wave: rows first .. first + 16*QT - 1 (those
 // before `last`), which are rows `at` and on of the tile; to the output where
-// the unit is whole, else to the slot's RT rows.
+// the unit is whole, else to the slot's RT rows.  (No store has a scalar
+// offset: after a 16-byte store with one, the compiler lets the next
+// instruction overwrite the stored registers, and gfx950 then stored the new
+// values of the last lanes.)
 template <int DT, int D, int QT, int RT>
 __device__ __forceinline__ void store_rows(const Seq& sq, State<D, QT>& st, uint32_t head, uint32_t first,
                                            uint32_t last, uint32_t at, bool whole, uint32_t slot) {
@@ -428,12 +431,12 @@ __device__ __forceinline__ void store_rows(const Seq& sq, State<D, QT>& st, uint
       if (whole) {
         const u32x4 v = {pack16<DT>(o[0][0] * f, o[1][0] * f), pack16<DT>(o[0][1] * f, o[1][1] * f),
                          pack16<DT>(o[0][2] * f, o[1][2] * f), pack16<DT>(o[0][3] * f, o[1][3] * f)};
-        __builtin_amdgcn_raw_buffer_store_b128(v, ro, ro_at + g * 16, jj * 64, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(v, ro, ro_at + g * 16 + jj * 64, 0, 0);
       } else {
         const f32x4 x = f32x4{o[0][0], o[1][0], o[0][1], o[1][1]} * f, y = f32x4{o[0][2], o[1][2], o[0][3], o[1][3]} * f;
-        const uint32_t to = m16 * D * 4 + g * 32, k = t * 16 * D * 4 + jj * 128;
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), rp, to, k, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), rp, to, k + 16, 0);
+        const uint32_t to = m16 * D * 4 + g * 32 + t * 16 * D * 4 + jj * 128;
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), rp, to, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), rp, to + 16, 0, 0);
       }
     }
     if (g == 0) {
