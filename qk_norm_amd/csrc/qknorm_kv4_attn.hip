@@ -857,7 +857,7 @@ __global__ __launch_bounds__(256, waves_per_simd(D, QT)) void kv4_attn_kernel(Kv
                   uint32_t slot) { run_unit<DT, D, QT, 1>(sq, b, tile, head, off, seg, whole, slot, nullptr); });
 }
 
-// Short sequences: a block a unit, its pages shared by W waves, one launch.
+// A block a unit, its pages shared by W waves, one launch.
 template <int DT, int D, int QT, int W>
 __global__ __launch_bounds__(64 * W, D * QT <= 64 ? 3 : (W > 4 ? 2 : waves_per_simd(D, QT))) void kv4_attn_block_kernel(Kv4AttnK) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -1009,6 +1009,8 @@ hipError_t launch_blocks(const Kv4AttnK& k, hipStream_t s) {
 template <int DT, int D, int QT>
 hipError_t launch(const Kv4AttnK& k, int block, hipStream_t s) {
   if (block == 4) return launch_blocks<DT, D, QT, 4>(k, s);
+  if constexpr (QT == 2)
+    if (block == 1) return launch_blocks<DT, D, QT, 1>(k, s);
   if constexpr (QT == 1)
     if (block == 8) return launch_blocks<DT, D, QT, 8>(k, s);
   hipLaunchKernelGGL((kv4_attn_kernel<DT, D, QT>), dim3(k.workers / 4), dim3(256), plan_lds(k.B), s, k);
@@ -1027,17 +1029,21 @@ hipError_t launch(const Kv4AttnK& k, int block, hipStream_t s) {
 // 8.5 (2000 tokens: 9.6 / 12.7), for 16 of 1000 13.7 / 9.6, for 64 of 500 19.3 /
 // 11.0, for 64 of up to 2000 19.5 / 19.9, for 64 of up to 8192 31.4 / 62; chunks of
 // 512 rows over 4096 tokens, four: 171 / 162, over up to 5000 81.5 / 66; 256 rows
-// over 4000 39.6 / 31.7; 64 rows over 4000 24.8 / 31.0.  From two units a wave on runs
-// are whole units themselves: eight prompts of 1000 tokens 169 / 188.
+// over 4000 39.6 / 31.7; 64 rows over 4000 24.8 / 31.0.  Where
+// units of two tiles outnumber the waves that the chip holds, a wave each, given
+// out by the hardware as others end (whole units in runs / blocks of four / of
+// one: eight prompts of 1000 tokens 169 / 188 / 113, one of 4096 198 / 191 / 167;
+// four of 300 36 / 27 / 17; but chunks over up to 5000, with as many units as
+// waves, 81.5 / 66 / 137).
 int block_waves(int tile, int64_t units, int64_t pages, int64_t workers) {
   if (tile == 16) {
     const int64_t most = units / 10 < 16 ? 16 : (units / 10 > 32 ? 32 : units / 10);
     if (pages > most) return 0;
-    // (16 of 1000: four waves 10.7; 64 of 500: eight waves 14.4)
+    // (16 of 1000 with four waves 10.7, 64 of 500 with eight 14.4)
     return pages > 4 && units <= 384 ? 8 : 4;
   }
-  const int64_t most = units / 4 > 128 ? 128 : units / 4;
-  return pages <= most && units < 2 * workers ? 4 : 0;
+  if (units >= 2 * workers || (units >= workers * 5 / 4 && pages <= 512) || (units >= workers / 2 && pages <= 8)) return 1;
+  return pages <= (units / 4 > 128 ? 128 : units / 4) ? 4 : 0;
 }
 
 // How a call is run: rows a tile, and how many waves take runs of page

@@ -422,3 +422,34 @@ def test_short_sequences(B, length, new, hkv, D):
     check(got, lse, rows, cache, table, lens, starts, hq, hkv, D, dtype)
     again, _ = run(rows, cache, table, lens, starts, hq, hkv, D, dtype, want_lse=False)
     assert torch.equal(got, again)
+
+
+def check_rows(got, lse, some, rows, cache, table, hq, hkv, D, dtype):
+    """Rows of one prompt that begins the cache, each as the last token of its own prefix."""
+    for i in some:
+        o, l, tol, ltol, _ = attention(rows[i:i + 1], cache, table, [i + 1], [0, 1], hq, hkv, D, D ** -0.5, 0, dtype)
+        assert bool(((got[i:i + 1].double() - o).abs() <= tol).all()), i
+        assert bool(((lse[i:i + 1].double() - l).abs() <= ltol).all()), i
+    assert bool(torch.isfinite(got).all()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("D,dtype", [(64, HF), (128, BF)])
+def test_prompt_of_a_wave_a_unit(D, dtype):
+    heads, n = 64, 500
+    print(f"[kv attention] prompt of 64 heads D={D}", flush=True)
+    rows, cache, table, starts = make([n], [n], heads, heads, D, dtype, D)
+    got, lse = run(rows, cache, table, [n], starts, heads, heads, D, dtype)
+    check_rows(got, lse, [0, 31, 32, 100, 499], rows, cache, table, heads, heads, D, dtype)
+
+
+def test_many_prompts():
+    # more than 64 sequences, and more units of two row tiles than twice the waves
+    hq, hkv, D, B, new = 32, 8, 256, 70, 40
+    print("[kv attention] 70 prompts", flush=True)
+    lens = [40 + (7 * i) % 50 for i in range(B)]
+    rows, cache, table, starts = make(lens, [new] * B, hq, hkv, D, BF, 77)
+    got, lse = run(rows, cache, table, lens, starts, hq, hkv, D, BF)
+    for b in (0, 37, 69):
+        lo, hi = starts[b], starts[b + 1]
+        check(got[lo:hi], lse[lo:hi], rows[lo:hi], cache, table[b:b + 1], lens[b:b + 1], [0, new], hq, hkv, D, BF)
+    assert bool(torch.isfinite(got).all()) and bool(torch.isfinite(lse).all())
